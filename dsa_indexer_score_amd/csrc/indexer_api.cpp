@@ -14,7 +14,12 @@
 #include <vector>
 
 #include "dsa_indexer.h"
+#include "host_common.h"
 #include "kernels.h"
+
+using dsai::DeviceGuard;
+using dsai::aligned;
+using dsai::fail_hip;
 
 struct indexer_s {
     indexer_config cfg;
@@ -26,12 +31,6 @@ namespace {
 thread_local std::string g_hip_error;
 thread_local std::string g_detail;  // why the last IDX_EWORKSPACE was returned, if known
 thread_local std::string g_msg;
-
-int fail_hip(hipError_t e)
-{
-    g_hip_error = hipGetErrorString(e);
-    return IDX_EHIP;
-}
 
 constexpr int kAllFlags = IDX_EXPAND | IDX_TAIL | IDX_SCREEN | IDX_FP8_MFMA;
 constexpr int64_t kMaxSel = 16000;  // 16-bit histogram counters bound the buffer at 65535
@@ -176,27 +175,17 @@ int64_t workspace_need(const indexer_config &cfg, int64_t S, int64_t T, int H, i
                         use_screen(cfg, H)).bytes;
 }
 
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    hipError_t err = hipSuccess;
-    explicit DeviceGuard(int dev)
-    {
-        err = hipGetDevice(&prev);
-        if (err == hipSuccess && prev != dev) {
-            err = hipSetDevice(dev);
-            changed = err == hipSuccess;
-        }
-    }
-    ~DeviceGuard()
-    {
-        if (changed) (void)hipSetDevice(prev);
-    }
-};
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 }  // namespace
+
+namespace dsai {
+
+int fail_hip(hipError_t e)
+{
+    g_hip_error = hipGetErrorString(e);
+    return IDX_EHIP;
+}
+
+}  // namespace dsai
 
 extern "C" {
 
