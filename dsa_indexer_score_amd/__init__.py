@@ -1,6 +1,8 @@
 """MI355X-native lightning indexer (DSA / CSA): scores, streaming top-k and
-the adjacent-pair overlap diagnostic, all computed by HIP kernels for gfx950
-behind the C ABI of include/dsa_indexer.h.
+the adjacent-pair overlap diagnostic, and the paged key/value cache that the
+selection reads (KVCache: append, attention, attention over selected
+positions), all computed by HIP kernels for gfx950 behind the C ABI of
+include/dsa_indexer.h.
 
 This module only marshals arguments: it checks tensor dtypes, shapes and
 devices, allocates outputs and the workspace through PyTorch, and passes raw
@@ -17,8 +19,9 @@ import torch
 from . import _lib
 from ._lib import (IDX_BF16, IDX_EXPAND, IDX_F32, IDX_FP8_E4M3, IDX_FP8_MFMA,  # noqa: F401
                    IDX_SCREEN, IDX_TAIL)
+from .kv import KVCache
 
-__all__ = ["Indexer", "score_topk", "output_width", "pair_overlap", "overlap_summary",
+__all__ = ["Indexer", "KVCache", "score_topk", "output_width", "pair_overlap", "overlap_summary",
            "library_path"]
 
 _DTYPE_CODE = {torch.float32: IDX_F32, torch.bfloat16: IDX_BF16,

@@ -26,8 +26,28 @@ class OverlapStats(ctypes.Structure):
                 ("frac_ge_75", ctypes.c_double), ("frac_ge_80", ctypes.c_double)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("device", ctypes.c_int), ("heads", ctypes.c_int),
+                ("d", ctypes.c_int), ("page", ctypes.c_int), ("pages", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class KvSeqs(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int), ("nseq", ctypes.c_int)]
+
+
+class KvRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 # name -> (restype, argtypes); mirrors include/dsa_indexer.h
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F, _PC, _PS, _PR = ctypes.c_float, ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), \
+    ctypes.POINTER(KvRows)
 SIGNATURES = {
     "indexer_create": (_I, [ctypes.POINTER(IndexerConfig), _I, ctypes.POINTER(_P)]),
     "indexer_destroy": (_I, [_P]),
@@ -48,6 +68,13 @@ SIGNATURES = {
     "indexer_overlap_summary": (_I, [_P, _P, _I64, ctypes.POINTER(OverlapStats)]),
     "indexer_screen_certificates": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _I, _P, _I64, _I, _I,
                                          _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "indexer_kv_append": (_I, [_PC, _PS, _PR, _PR, _I64, _P, _P, _I64, _I, _I, _PR, _I, _PR, _P]),
+    "indexer_kv_attend": (_I, [_PC, _PS, _PR, _I64, _I, _F, _I, _I64, _P, _P, _P, _SZ, _P]),
+    "indexer_kv_attend_workspace_bytes": (_I, [_PC, _PS, _I64, _I, _I64, ctypes.POINTER(_SZ)]),
+    "indexer_kv_attend_selected": (_I, [_PC, _PS, _PR, _I64, _I, _F, _P, _I, _P, _P, _P, _P, _P,
+                                        _SZ, _P]),
+    "indexer_kv_attend_selected_workspace_bytes": (_I, [_PC, _PS, _I64, _I, _I,
+                                                        ctypes.POINTER(_SZ)]),
     "indexer_strerror": (ctypes.c_char_p, [_I]),
     "indexer_source_hash": (ctypes.c_char_p, []),
 }

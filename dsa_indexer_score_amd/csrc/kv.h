@@ -1,0 +1,70 @@
+// Launch interface of the paged key/value cache: append and attention.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dsai {
+
+// The cache and the sequences in it, as the kernels read them.  Rows of d
+// elements are numbered (page * heads + head) * page_size + slot.
+struct KvCache {
+    void *k, *v;              // [pages, heads, page, d] bf16 or e4m3
+    float *k_scale, *v_scale; // [pages, heads], e4m3 only
+    uint32_t pages;
+    int heads;
+    int page_shift;           // log2 of the tokens per page
+    const int32_t *cu;        // [nseq + 1] rows of this call, packed
+    const int32_t *seq_len;   // [nseq]
+    const int32_t *table;     // page ids, sequence i at table + i * table_stride
+    int64_t table_stride;
+    int table_width;
+    int nseq;
+};
+
+struct KvAppendParams {
+    KvCache c;
+    const uint16_t *src[3];   // k, v, q: bf16, strides in elements
+    int64_t tok_stride[3], head_stride[3];
+    uint16_t *q_out;
+    int64_t qo_tok, qo_head;
+    const float *cos, *sin;   // [rope_rows, rot / 2], or null: no rotation
+    int64_t rope_rows;
+    int rot, interleaved;
+    int q_heads;              // 0: no queries
+    int64_t N;                // new tokens
+    int64_t kv_units, q_units;
+};
+
+struct KvAttendParams {
+    KvCache c;
+    const uint16_t *q;        // bf16, [S, q_heads, d] with strides in elements
+    int64_t q_tok, q_head;
+    int64_t S;
+    int q_heads, group;       // query heads in all, and per key head
+    float c2;                 // softmax scale * log2(e)
+    int causal;
+    uint16_t *out;            // [S, q_heads, d] bf16
+    float *lse;               // [S, q_heads] or null
+    // selected positions: row t's entries at idx + t * W, valid_len[t] of them
+    const int32_t *idx;
+    int W;
+    const int32_t *valid_len;
+    const int32_t *idx0;      // [nseq] or null, subtracted from the entries
+    // the split: `chunk` keys a block, nsplit blocks along the keys; rows that
+    // need more than one leave (o, m, l) in part_o / part_ml for the join
+    int tile_rows;            // query rows of a sequence that one block takes
+    int64_t slots;            // row tiles, empty ones among them
+    int chunk, nsplit;
+    float *part_o;            // [nsplit, S, q_heads, d]
+    float2 *part_ml;          // [nsplit, S, q_heads]
+};
+
+hipError_t launch_kv_append(int dtype, int d, const KvAppendParams &p, hipStream_t st);
+
+// mt: 16-column tiles of query rows x heads per block (1..4)
+hipError_t launch_kv_rows(int dtype, int d, int mt, const KvAttendParams &p, hipStream_t st);
+hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st);
+
+constexpr int kKvHeadTile = 64;   // query heads of one key head that a block takes at most
+
+}  // namespace dsai

@@ -1,0 +1,314 @@
+// Host side of the paged key/value cache's C ABI (include/dsa_indexer.h):
+// argument checks, the split along the keys, workspace sizes and launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "dsa_indexer.h"
+#include "host_common.h"
+#include "kv.h"
+
+namespace {
+
+using dsai::aligned;
+using dsai::DeviceGuard;
+using dsai::fail_hip;
+
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t div_up(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+int log2_page(int page)
+{
+    for (int s = 4; s <= 7; ++s)
+        if (page == 1 << s) return s;
+    return -1;
+}
+
+int check_cache(const indexer_kv_cache *c)
+{
+    if (!c || c->device < 0 || c->heads < 1 || c->d < 1 || c->page < 1 || c->pages < 1)
+        return IDX_EINVAL;
+    if (c->dtype != IDX_F32 && c->dtype != IDX_BF16 && c->dtype != IDX_FP8_E4M3) return IDX_EINVAL;
+    if (c->dtype == IDX_F32 || (c->d != 64 && c->d != 128) || log2_page(c->page) < 0)
+        return IDX_EUNSUPPORTED;
+    if (c->pages > INT32_MAX || c->heads > 65535 ||
+        c->pages * c->heads >= (int64_t)UINT32_MAX / c->page)
+        return IDX_EUNSUPPORTED;  // rows are numbered in 32 bits
+    const bool fp8 = c->dtype == IDX_FP8_E4M3;
+    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return IDX_EINVAL;
+    if (fp8 ? !c->k_scale || !c->v_scale : c->k_scale || c->v_scale) return IDX_EINVAL;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return IDX_EINVAL;
+    return IDX_OK;
+}
+
+// Sizes only: what the workspace functions may look at.
+int check_seq_sizes(const indexer_kv_cache *c, const indexer_kv_seqs *s, int64_t rows)
+{
+    if (!s || s->nseq < 0 || s->table_width < 0 || rows < 0) return IDX_EINVAL;
+    if (s->nseq > 0 && s->table_stride < s->table_width) return IDX_EINVAL;
+    if (rows + 2 * (int64_t)s->nseq >= INT32_MAX ||
+        (int64_t)s->table_width * c->page >= INT32_MAX)
+        return IDX_EUNSUPPORTED;
+    return IDX_OK;
+}
+
+int check_seqs(const indexer_kv_cache *c, const indexer_kv_seqs *s, int64_t rows)
+{
+    const int rc = check_seq_sizes(c, s, rows);
+    if (rc != IDX_OK) return rc;
+    if (s->nseq > 0 && (!s->cu_q || !s->seq_len || (s->table_width > 0 && !s->table)))
+        return IDX_EINVAL;
+    if (!aligned(s->cu_q, 4) || !aligned(s->seq_len, 4) || !aligned(s->table, 4)) return IDX_EINVAL;
+    return IDX_OK;
+}
+
+// Rows of bf16 that the kernels read (or write) 16 bytes at a time.
+bool rows_ok(const indexer_kv_rows *r)
+{
+    return r && r->ptr && aligned(r->ptr, 16) && r->row_stride >= 0 && r->head_stride >= 0 &&
+           r->row_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+
+// Rows that are written must not share memory: one stride spans the other.
+bool rows_apart(const indexer_kv_rows *r, int64_t rows, int64_t heads, int64_t d)
+{
+    if (rows <= 1) return heads <= 1 || r->head_stride >= d;
+    if (heads <= 1) return r->row_stride >= d;
+    return (r->head_stride >= d && r->row_stride >= (heads - 1) * r->head_stride + d) ||
+           (r->row_stride >= d && r->head_stride >= (rows - 1) * r->row_stride + d);
+}
+
+dsai::KvCache kernel_cache(const indexer_kv_cache *c, const indexer_kv_seqs *s)
+{
+    dsai::KvCache k{};
+    k.k = c->k;
+    k.v = c->v;
+    k.k_scale = c->k_scale;
+    k.v_scale = c->v_scale;
+    k.pages = (uint32_t)c->pages;
+    k.heads = c->heads;
+    k.page_shift = log2_page(c->page);
+    k.cu = s->cu_q;
+    k.seq_len = s->seq_len;
+    k.table = s->table;
+    k.table_stride = s->table_stride;
+    k.table_width = s->table_width;
+    k.nseq = s->nseq;
+    return k;
+}
+
+// How a call is cut into blocks; depends on host sizes only, so that the
+// workspace functions and the calls agree.
+struct Plan {
+    int nt, tile_rows, nsplit, chunk;
+    int64_t slots, part_ml, bytes;
+};
+
+constexpr int64_t kFillBlocks = 512;  // two blocks for each CU
+constexpr int64_t kMinChunk = 256;    // keys that are worth a block of four waves
+
+Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int64_t max_len,
+               bool selected)
+{
+    Plan p{};
+    const int group = q_heads / c->heads, gsize = std::min(group, dsai::kKvHeadTile);
+    const int64_t ngrp = div_up(group, dsai::kKvHeadTile);
+    const int64_t rows = selected ? 1 : div_up(S, std::max(nseq, 1));  // of a sequence, on average
+    const int64_t cols = std::min<int64_t>(std::max<int64_t>(1, dsai::kKvHeadTile / gsize),
+                                           std::max<int64_t>(rows, 1)) * gsize;
+    p.nt = (int)div_up(cols, 16);
+    p.tile_rows = selected ? 1 : std::max(1, 16 * p.nt / gsize);
+    p.slots = selected ? S : S / p.tile_rows + nseq;
+    const int64_t units = std::max<int64_t>(1, selected ? S : std::max<int64_t>(S / p.tile_rows, 1)) *
+                          c->heads * ngrp;
+    const int64_t want = std::max<int64_t>(1, kFillBlocks / units);
+    int64_t chunk = std::max(kMinChunk, round_up(div_up(std::max<int64_t>(max_len, 1), want), 128));
+    int64_t nsplit = div_up(std::max<int64_t>(max_len, 1), chunk);
+    if (nsplit <= 1) nsplit = 1, chunk = INT32_MAX;
+    p.nsplit = (int)nsplit;
+    p.chunk = (int)chunk;
+    if (nsplit > 1) {
+        p.part_ml = round_up(nsplit * S * q_heads * c->d * 4, 256);
+        p.bytes = p.part_ml + nsplit * S * q_heads * 8;
+    }
+    return p;
+}
+
+int check_attend_sizes(const indexer_kv_cache *c, const indexer_kv_seqs *s, int64_t S, int q_heads)
+{
+    int rc = check_cache(c);
+    if (rc != IDX_OK) return rc;
+    rc = check_seq_sizes(c, s, S);
+    if (rc != IDX_OK) return rc;
+    if (q_heads < 1 || q_heads % c->heads) return IDX_EINVAL;
+    if (S * (int64_t)q_heads >= INT32_MAX) return IDX_EUNSUPPORTED;
+    return IDX_OK;
+}
+
+int64_t most_keys(const indexer_kv_cache *c, const indexer_kv_seqs *s, int64_t max_len)
+{
+    const int64_t cap = (int64_t)s->table_width * c->page;
+    return max_len > 0 && max_len < cap ? max_len : cap;
+}
+
+int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv_rows *q,
+           int64_t S, int q_heads, float scale, int causal, int64_t max_len, const int32_t *idx,
+           int W, const int32_t *valid_len, const int32_t *idx0, void *out, float *lse,
+           void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc = check_attend_sizes(c, s, S, q_heads);
+    if (rc != IDX_OK) return rc;
+    rc = check_seqs(c, s, S);
+    if (rc != IDX_OK) return rc;
+    if (!std::isfinite(scale)) return IDX_EINVAL;
+    if (S == 0 || s->nseq == 0) return IDX_OK;  // no row belongs to a sequence
+    if (!rows_ok(q) || !out || !aligned(out, 16) || !aligned(lse, 4)) return IDX_EINVAL;
+    const Plan pl = make_plan(c, S, q_heads, s->nseq, idx ? W : most_keys(c, s, max_len),
+                              idx != nullptr);
+    const int64_t blocks = pl.slots * pl.nsplit * c->heads *
+                           div_up(q_heads / c->heads, dsai::kKvHeadTile);
+    if (blocks >= INT32_MAX) return IDX_EUNSUPPORTED;
+    if (pl.bytes > 0 && (!workspace || workspace_bytes < (size_t)pl.bytes || !aligned(workspace, 16)))
+        return IDX_EWORKSPACE;
+
+    DeviceGuard guard(c->device);
+    if (guard.err != hipSuccess) return fail_hip(guard.err);
+    dsai::KvAttendParams p{};
+    p.c = kernel_cache(c, s);
+    p.q = static_cast<const uint16_t *>(q->ptr);
+    p.q_tok = q->row_stride;
+    p.q_head = q->head_stride;
+    p.S = S;
+    p.q_heads = q_heads;
+    p.group = q_heads / c->heads;
+    p.c2 = (float)((double)scale * 1.4426950408889634074);
+    p.causal = causal;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.idx = idx;
+    p.W = W;
+    p.valid_len = valid_len;
+    p.idx0 = idx0;
+    p.tile_rows = pl.tile_rows;
+    p.slots = pl.slots;
+    p.chunk = pl.chunk;
+    p.nsplit = pl.nsplit;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + pl.part_ml);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = dsai::launch_kv_rows(c->dtype, c->d, pl.nt, p, st);
+    if (e != hipSuccess) return fail_hip(e);
+    if (pl.nsplit > 1) {
+        e = dsai::launch_kv_join(c->d, p, st);
+        if (e != hipSuccess) return fail_hip(e);
+    }
+    return IDX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int indexer_kv_append(const indexer_kv_cache *c, const indexer_kv_seqs *s,
+                      const indexer_kv_rows *k, const indexer_kv_rows *v, int64_t N,
+                      const float *cos, const float *sin, int64_t rope_rows, int rot,
+                      int interleaved, const indexer_kv_rows *q, int q_heads,
+                      const indexer_kv_rows *q_out, void *stream)
+{
+    int rc = check_cache(c);
+    if (rc != IDX_OK) return rc;
+    rc = check_seqs(c, s, N);
+    if (rc != IDX_OK) return rc;
+    if (interleaved != 0 && interleaved != 1) return IDX_EINVAL;
+    if (!cos != !sin) return IDX_EINVAL;
+    if (cos) {
+        if (rot < 2 || rot > c->d || rope_rows < 1) return IDX_EINVAL;
+        if (rot % 16) return IDX_EUNSUPPORTED;
+        if (!aligned(cos, 16) || !aligned(sin, 16)) return IDX_EINVAL;
+    }
+    if (q_heads < 0 || (q_heads > 0 && (!q || !q_out))) return IDX_EINVAL;
+    if (N == 0 || s->nseq == 0) return IDX_OK;
+    if (!rows_ok(k) || !rows_ok(v)) return IDX_EINVAL;
+    if (q_heads > 0 && (!rows_ok(q) || !rows_ok(q_out) || !rows_apart(q_out, N, q_heads, c->d)))
+        return IDX_EINVAL;
+
+    dsai::KvAppendParams p{};
+    p.c = kernel_cache(c, s);
+    const indexer_kv_rows *src[3] = {k, v, q_heads > 0 ? q : nullptr};
+    for (int i = 0; i < 3; ++i) {
+        if (!src[i]) continue;
+        p.src[i] = static_cast<const uint16_t *>(src[i]->ptr);
+        p.tok_stride[i] = src[i]->row_stride;
+        p.head_stride[i] = src[i]->head_stride;
+    }
+    if (q_heads > 0) {
+        p.q_out = static_cast<uint16_t *>(q_out->ptr);
+        p.qo_tok = q_out->row_stride;
+        p.qo_head = q_out->head_stride;
+    }
+    p.cos = cos;
+    p.sin = sin;
+    p.rope_rows = rope_rows;
+    p.rot = cos ? rot : 0;
+    p.interleaved = interleaved;
+    p.q_heads = q_heads;
+    p.N = N;
+    // A sequence of n new tokens touches at most n / page + 2 pages; with
+    // page slots numbered from cu / page + 2 i, sequence i has that many.
+    p.kv_units = (N / c->page + 2 * (int64_t)s->nseq) * c->heads * 2;
+    p.q_units = q_heads > 0 ? N : 0;
+    if (p.kv_units + p.q_units >= INT32_MAX) return IDX_EUNSUPPORTED;
+    DeviceGuard guard(c->device);
+    if (guard.err != hipSuccess) return fail_hip(guard.err);
+    const hipError_t e = dsai::launch_kv_append(c->dtype, c->d, p, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? IDX_OK : fail_hip(e);
+}
+
+int indexer_kv_attend_workspace_bytes(const indexer_kv_cache *c, const indexer_kv_seqs *s,
+                                      int64_t S, int q_heads, int64_t max_len, size_t *bytes)
+{
+    if (!bytes || max_len < 0) return IDX_EINVAL;
+    const int rc = check_attend_sizes(c, s, S, q_heads);
+    if (rc != IDX_OK) return rc;
+    *bytes = S > 0 && s->nseq > 0
+                 ? (size_t)make_plan(c, S, q_heads, s->nseq, most_keys(c, s, max_len), false).bytes
+                 : 0;
+    return IDX_OK;
+}
+
+int indexer_kv_attend(const indexer_kv_cache *c, const indexer_kv_seqs *s,
+                      const indexer_kv_rows *q, int64_t S, int q_heads, float scale, int causal,
+                      int64_t max_len, void *out, float *lse, void *workspace,
+                      size_t workspace_bytes, void *stream)
+{
+    if (max_len < 0 || (causal != 0 && causal != 1)) return IDX_EINVAL;
+    return attend(c, s, q, S, q_heads, scale, causal, max_len, nullptr, 0, nullptr, nullptr, out,
+                  lse, workspace, workspace_bytes, stream);
+}
+
+int indexer_kv_attend_selected_workspace_bytes(const indexer_kv_cache *c, const indexer_kv_seqs *s,
+                                               int64_t S, int q_heads, int W, size_t *bytes)
+{
+    if (!bytes || W < 1) return IDX_EINVAL;
+    const int rc = check_attend_sizes(c, s, S, q_heads);
+    if (rc != IDX_OK) return rc;
+    *bytes = S > 0 && s->nseq > 0 ? (size_t)make_plan(c, S, q_heads, s->nseq, W, true).bytes : 0;
+    return IDX_OK;
+}
+
+int indexer_kv_attend_selected(const indexer_kv_cache *c, const indexer_kv_seqs *s,
+                               const indexer_kv_rows *q, int64_t S, int q_heads, float scale,
+                               const int32_t *idx, int W, const int32_t *valid_len,
+                               const int32_t *idx0, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    if (W < 1 || !idx || !valid_len || !aligned(idx, 4) || !aligned(valid_len, 4) ||
+        !aligned(idx0, 4))
+        return IDX_EINVAL;
+    return attend(c, s, q, S, q_heads, scale, 0, 0, idx, W, valid_len, idx0, out, lse, workspace,
+                  workspace_bytes, stream);
+}
+
+}  // extern "C"

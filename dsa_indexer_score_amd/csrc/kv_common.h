@@ -1,0 +1,57 @@
+// Device helpers shared by the paged cache's kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kv.h"
+
+namespace dsai {
+namespace {
+
+typedef __bf16 kvb8 __attribute__((ext_vector_type(8)));
+typedef __bf16 kvb2 __attribute__((ext_vector_type(2)));
+typedef float kvf4 __attribute__((ext_vector_type(4)));
+
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Two floats to packed bf16, round to nearest even.
+__device__ inline uint32_t pack_bf16(float a, float b)
+{
+    kvb2 v;
+    v[0] = (__bf16)a;
+    v[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ inline int clamped(int x, int64_t hi)
+{
+    return x < 0 ? 0 : (int64_t)x > hi ? (int)hi : x;
+}
+
+// The largest i in [0, n) with max(cu[i], 0) / div + mul * i <= slot, by the
+// whole wave: 64 probes a step, so one load for up to 64 sequences.  For an
+// array that does not ascend the answer is some i in [0, n).
+__device__ inline int find_seq(const int32_t *cu, int n, int64_t slot, int div, int mul)
+{
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64;
+        const int64_t i = lo + (int64_t)lane * step;
+        const bool in = i < hi;
+        const int at = in ? (int)i : lo;
+        const int x = cu[at];
+        const bool ok = in && (int64_t)((x < 0 ? 0 : x) / div) + (int64_t)mul * at <= slot;
+        int cnt = __popcll(__ballot(ok));
+        cnt = cnt < 1 ? 1 : cnt;
+        lo += (cnt - 1) * step;
+        if (lo >= hi) lo = hi - 1;
+        hi = hi - lo < step ? hi : lo + step;
+        lo = uniform(lo);
+        hi = uniform(hi);
+    }
+    return lo;
+}
+
+}  // namespace
+}  // namespace dsai

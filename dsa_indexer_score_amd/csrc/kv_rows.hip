@@ -1,0 +1,543 @@
+// kv_rows: attention of a few query rows over the paged cache, all of a
+// sequence's keys or the positions selected for the row.
+//
+//   o = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+//
+// One pass over the keys with the running maximum m and sum l of each row; the
+// scores are kept in base 2 (scale * log2 e, times the key page's scale, is one
+// fp32 factor on the exact bf16 products that the matrix unit sums in fp32).
+//
+// A block takes the query rows of one key head (up to 64 columns: rows of a
+// sequence times the head's query heads) and a range of the keys; its four
+// waves take turns at tiles of 32 keys, each with a softmax state of its own,
+// joined through LDS at the end.  Nothing but the list of key rows is shared in
+// the loop, so there is no barrier in it: keys and values go from memory to
+// registers and from there to the matrix unit.  Both products are computed
+// transposed, S^T = K Q^T and O^T = V^T P^T:
+//  - the keys are the rows of A; lane (m, g) reads 16-byte chunks of key m, and
+//    the contraction takes the channels in the order in which they come;
+//  - S^T leaves lane (n, g) with the scores of column n against keys 4 g + i of
+//    both halves of the tile, which is the B operand of the second product when
+//    the contraction takes the keys in that order: P never leaves its lane;
+//  - V^T needs, for a channel, the values of those eight keys: lane (m, g) reads
+//    D / 16 neighbouring channels of each of them and transposes bytes
+//    (v_perm), then widens the codes exactly to bf16.
+// P is rounded to bf16 for the matrix unit after it took the value page's scale
+// (relative 2^-9, as the rounding of the output); l sums the unrounded
+// probabilities.
+//
+// Blocks that share a row (more keys than one chunk) write (o, m, l) to the
+// workspace and kv_join adds them up; the order is fixed, so results repeat.
+#include "kv_common.h"
+
+namespace dsai {
+namespace {
+
+constexpr int kList = 1024;             // keys resolved to rows at a time
+constexpr uint32_t kNoRow = 0xffffffffu;
+constexpr float kLn2 = 0.693147180559945309f;
+
+template <int N> struct Words;          // N dwords that one load brings
+template <> struct Words<1> { using T = uint32_t; };
+template <> struct Words<2> { using T = uint2; };
+template <> struct Words<4> { using T = uint4; };
+
+__device__ inline uint32_t word(uint32_t x, int) { return x; }
+__device__ inline uint32_t word(const uint2 &x, int i) { return i ? x.y : x.x; }
+__device__ inline uint32_t word(const uint4 &x, int i)
+{
+    return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+}
+__device__ inline void clear(uint32_t &x) { x = 0; }
+__device__ inline void clear(uint2 &x) { x = make_uint2(0, 0); }
+__device__ inline void clear(uint4 &x) { x = make_uint4(0, 0, 0, 0); }
+
+template <bool HI> __device__ inline uint32_t widen2(uint32_t w)
+{
+    auto v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel)
+{
+    return __builtin_amdgcn_perm(hi, lo, sel);  // bytes 0-3 from lo, 4-7 from hi
+}
+
+// What a lane reads of a tile of 32 keys.
+template <bool FP8, int D> struct Tile {
+    static constexpr int ES = FP8 ? 1 : 2;
+    static constexpr int KU = D * ES / 64;          // 16-byte chunks of a key
+    static constexpr int KS = D / 32;               // contraction steps of S
+    static constexpr int VW = D * ES / 64;          // dwords of D / 16 channels
+    static constexpr int MT = D / 16;               // 16-channel tiles of O
+    using VT = typename Words<VW>::T;
+    uint4 k[2][KU];
+    VT v[8];
+
+    __device__ void load(const char *kb, const char *vb, const uint32_t *list, int m, int g)
+    {
+        constexpr uint32_t RB = D * ES;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t row = list[16 * t + m];
+            const uint4 *p = reinterpret_cast<const uint4 *>(
+                kb + (uint64_t)(row == kNoRow ? 0 : row) * RB) + g;
+#pragma unroll
+            for (int u = 0; u < KU; ++u) k[t][u] = p[4 * u];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t row = list[16 * (j >> 2) + 4 * g + (j & 3)];
+            v[j] = *reinterpret_cast<const VT *>(vb + (uint64_t)(row == kNoRow ? 0 : row) * RB +
+                                                 m * (VW * 4));
+        }
+    }
+
+    __device__ kvb8 key(int t, int step) const
+    {
+        if constexpr (FP8) {
+            const uint4 &x = k[t][step >> 1];
+            const uint32_t a = step & 1 ? x.z : x.x, b = step & 1 ? x.w : x.y;
+            const uint4 w = make_uint4(widen2<false>(a), widen2<true>(a), widen2<false>(b),
+                                       widen2<true>(b));
+            return __builtin_bit_cast(kvb8, w);
+        } else {
+            return __builtin_bit_cast(kvb8, k[t][step]);
+        }
+    }
+
+    // Channel `t` of the lane's D / 16 for its eight keys, t = NT q .. NT q +
+    // NT - 1 (NT channels of one dword).
+    __device__ void values(int q, kvb8 *a) const
+    {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = word(v[j], q);
+        if constexpr (FP8) {
+            uint32_t o[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 4 x 4 bytes: keys x channels -> channels x keys
+                const uint32_t *x = w + 4 * h;
+                const uint32_t a0 = perm(x[1], x[0], 0x05010400), a1 = perm(x[1], x[0], 0x07030602);
+                const uint32_t b0 = perm(x[3], x[2], 0x05010400), b1 = perm(x[3], x[2], 0x07030602);
+                o[h][0] = perm(b0, a0, 0x05040100);
+                o[h][1] = perm(b0, a0, 0x07060302);
+                o[h][2] = perm(b1, a1, 0x05040100);
+                o[h][3] = perm(b1, a1, 0x07060302);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint4 y = make_uint4(widen2<false>(o[0][t]), widen2<true>(o[0][t]),
+                                           widen2<false>(o[1][t]), widen2<true>(o[1][t]));
+                a[t] = __builtin_bit_cast(kvb8, y);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t sel = t ? 0x07060302 : 0x05040100;
+                const uint4 y = make_uint4(perm(w[1], w[0], sel), perm(w[3], w[2], sel),
+                                           perm(w[5], w[4], sel), perm(w[7], w[6], sel));
+                a[t] = __builtin_bit_cast(kvb8, y);
+            }
+        }
+    }
+};
+
+template <bool FP8, int D, int NT, bool SEL>
+__global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendParams p)
+{
+    using TL = Tile<FP8, D>;
+    constexpr int MT = TL::MT, CH = FP8 ? 4 : 2;  // channels that one dword of values holds
+    constexpr int PITCH = D + 4;
+    struct List { uint32_t row[kList]; float ks[FP8 ? kList : 4], vs[FP8 ? kList : 4]; };
+    struct Join { float o[4][16][PITCH]; };
+    __shared__ union { List list; Join join; } sm;
+    __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
+
+    const KvCache &kc = p.c;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
+    const int n = lane & 15, g = lane >> 4;
+
+    // ---- which rows, key head, query heads and keys
+    int64_t b = blockIdx.x;
+    const int head = (int)(b % kc.heads);
+    b /= kc.heads;
+    const int gsize = p.group < kKvHeadTile ? p.group : kKvHeadTile;
+    const int ngrp = (p.group + kKvHeadTile - 1) / kKvHeadTile;
+    const int grp = (int)(b % ngrp);
+    b /= ngrp;
+    const int64_t slot = b % p.slots;
+    const int split = (int)(b / p.slots);
+
+    const int R = SEL ? 1 : p.tile_rows;
+    const int seq = SEL ? find_seq(kc.cu, kc.nseq, slot, 1, 0) : find_seq(kc.cu, kc.nseq, slot, R, 1);
+    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
+    const int rows_in_seq = c1 - c0;
+    const int64_t t0 = SEL ? slot - c0 : (slot - (c0 / R + (int64_t)seq)) * R;
+    if (t0 < 0 || t0 >= rows_in_seq) return;
+    const int ntok = (int)(rows_in_seq - t0 < R ? rows_in_seq - t0 : R);
+    const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+    const int64_t row0 = c0 + t0;
+    // entries: keys 0 .. entries of the sequence, or of the row's selection
+    int entries, base = 0;
+    if constexpr (SEL) {
+        entries = clamped(p.valid_len[row0], p.W);
+        base = p.idx0 ? p.idx0[seq] : 0;
+    } else {
+        const int64_t last = p.causal ? (int64_t)len - rows_in_seq + t0 + ntok : len;
+        entries = clamped(last < 0 ? 0 : (int)last, len);
+    }
+    const int e0 = split * p.chunk;
+    if (split > 0 && e0 >= entries) return;
+    const int e1 = entries - e0 < p.chunk ? entries : e0 + p.chunk;
+
+    // ---- the columns: query rows x heads
+    kvb8 q[NT][TL::KS];
+    int lim[NT];                 // keys that the column sees
+    int64_t orow[NT];            // its output row, or -1
+    int minlim = 0x7fffffff;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int col = 16 * t + n, tok = col / gsize, hh = grp * kKvHeadTile + col % gsize;
+        const bool in = tok < ntok && hh < p.group;
+        orow[t] = in ? (row0 + tok) * p.q_heads + head * p.group + hh : -1;
+        lim[t] = 0x7fffffff;
+        if constexpr (!SEL) {
+            if (in && p.causal) {
+                const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
+                lim[t] = x < 0 ? 0 : (int)x;
+            }
+        }
+        minlim = lim[t] < minlim ? lim[t] : minlim;
+        const uint16_t *src = p.q + (row0 + tok) * p.q_tok +
+                              (int64_t)(head * p.group + hh) * p.q_head;
+#pragma unroll
+        for (int s = 0; s < TL::KS; ++s) {
+            // the channels that the key operand of this step holds
+            const int at = FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (in) x = *reinterpret_cast<const uint4 *>(src + at);
+            q[t][s] = __builtin_bit_cast(kvb8, x);
+        }
+    }
+#pragma unroll
+    for (int s = 1; s < 16; s <<= 1) {
+        const int o = __shfl_xor(minlim, s);
+        minlim = o < minlim ? o : minlim;
+    }
+    minlim = uniform(minlim);
+
+    kvf4 o[NT][MT];
+    float mx[NT], l[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        mx[t] = -__builtin_inff();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[t][i] = kvf4{0, 0, 0, 0};
+    }
+
+    const char *kb = static_cast<const char *>(kc.k), *vb = static_cast<const char *>(kc.v);
+    const int page_mask = (1 << kc.page_shift) - 1;
+    const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
+
+    for (int s0 = e0; s0 < e1; s0 += kList) {
+        // ---- resolve up to kList entries to cache rows and their scales
+        const int cnt = e1 - s0 < kList ? e1 - s0 : kList;
+        const int padded = (cnt + 31) & ~31;
+        if (s0 > e0) __syncthreads();
+        for (int i = tid; i < padded; i += 256) {
+            uint32_t row = kNoRow;
+            float ks = 0.0f, vs = 0.0f;
+            if (i < cnt) {
+                int64_t pos = s0 + i;
+                if constexpr (SEL) pos = (int64_t)p.idx[row0 * p.W + pos] - base;
+                if (!SEL || (pos >= 0 && pos < len)) {
+                    const uint32_t id = (uint32_t)table[pos >> kc.page_shift];
+                    if (id < kc.pages) {
+                        const uint32_t unit = id * (uint32_t)kc.heads + head;
+                        row = (unit << kc.page_shift) + ((int)pos & page_mask);
+                        if constexpr (FP8) {
+                            ks = kc.k_scale[unit] * p.c2;
+                            vs = kc.v_scale[unit];
+                        }
+                    }
+                }
+            }
+            sm.list.row[i] = row;
+            if constexpr (FP8) {
+                sm.list.ks[i] = ks;
+                sm.list.vs[i] = vs;
+            }
+        }
+        __syncthreads();
+
+        // ---- tiles of 32 keys, in turn over the waves, the next one's loads ahead
+        TL cur, nxt;
+        int at = wave * 32;
+        if (at < padded) cur.load(kb, vb, sm.list.row + at, n, g);
+        for (; at < padded; at += 128) {
+            if (at + 128 < padded) nxt.load(kb, vb, sm.list.row + at + 128, n, g);
+            // keys that are not there: no score, and values that cannot be NaN
+            const uint32_t *list = sm.list.row + at;
+            const bool gaps = __ballot(list[n] == kNoRow || list[16 + n] == kNoRow) != 0;
+            if (gaps) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (list[16 * (j >> 2) + 4 * g + (j & 3)] == kNoRow) clear(cur.v[j]);
+            }
+            const bool edge = !SEL && s0 + at + 32 > minlim;
+            uint4 pk[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float x[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    kvf4 acc = {0, 0, 0, 0};
+#pragma unroll
+                    for (int s = 0; s < TL::KS; ++s)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cur.key(h, s), q[t][s], acc,
+                                                                      0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = 16 * h + 4 * g + i;
+                        x[4 * h + i] = acc[i] * (FP8 ? sm.list.ks[at + key] : p.c2);
+                        if (gaps && list[key] == kNoRow) x[4 * h + i] = -__builtin_inff();
+                        if (edge && s0 + at + key >= lim[t]) x[4 * h + i] = -__builtin_inff();
+                    }
+                }
+                float top = x[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (__ballot(top > mx[t])) {
+                    const float m2 = fmaxf(mx[t], top);
+                    const float a = mx[t] == m2 ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - m2);
+                    mx[t] = m2;
+                    l[t] *= a;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) o[t][i] *= a;
+                }
+                const float m1 = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = __builtin_amdgcn_exp2f(x[i] - m1);
+                    l[t] += x[i];
+                }
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] *= sm.list.vs[at + 16 * (i >> 2) + 4 * g + (i & 3)];
+                }
+                pk[t] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                   pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            }
+#pragma unroll
+            for (int w = 0; w < TL::VW; ++w) {
+                kvb8 a[CH];
+                cur.values(w, a);
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        o[t][CH * w + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            a[i], __builtin_bit_cast(kvb8, pk[t]), o[t][CH * w + i], 0, 0, 0);
+            }
+            cur = nxt;
+        }
+    }
+
+    // ---- join the waves
+    float f[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        l[t] += __shfl_xor(l[t], 16);
+        l[t] += __shfl_xor(l[t], 32);
+        if (g == 0) {
+            sm_m[wave][16 * t + n] = mx[t];
+            sm_l[wave][16 * t + n] = l[t];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int col = 16 * t + n;
+        const float m4 = fmaxf(fmaxf(sm_m[0][col], sm_m[1][col]), fmaxf(sm_m[2][col], sm_m[3][col]));
+        f[t] = mx[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mx[t] - m4);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        if (t > 0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < MT; w += 4) {
+                float4 x;
+                x.x = o[t][w][i] * f[t];
+                x.y = o[t][w + 1][i] * f[t];
+                x.z = o[t][w + 2][i] * f[t];
+                x.w = o[t][w + 3][i] * f[t];
+                *reinterpret_cast<float4 *>(&sm.join.o[wave][n][MT * (4 * g + i) + w]) = x;
+            }
+        __syncthreads();
+        // thread: column tid / 16, D / 16 channels
+        constexpr int C = D / 16;
+        const int cl = tid >> 4, ch = (tid & 15) * C, col = 16 * t + cl;
+        const int tok = col / gsize, hh = grp * kKvHeadTile + col % gsize;
+        if (tok < ntok && hh < p.group) {
+            float m4 = sm_m[0][col];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) m4 = fmaxf(m4, sm_m[w][col]);
+            float sum = 0.0f, y[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) y[j] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (sm_m[w][col] != -__builtin_inff())
+                    sum += sm_l[w][col] * __builtin_amdgcn_exp2f(sm_m[w][col] - m4);
+#pragma unroll
+                for (int j = 0; j < C; ++j) y[j] += sm.join.o[w][cl][ch + j];
+            }
+            const int64_t out = (row0 + tok) * p.q_heads + head * p.group + hh;
+            // the row's own keys decide whether other blocks have a part of it
+            int own = entries;
+            if constexpr (!SEL) {
+                if (p.causal) {
+                    const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
+                    own = x < 0 ? 0 : (int)x;
+                }
+            }
+            if (own <= p.chunk) {
+                if (split == 0) {
+                    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < C; j += 2)
+                        *reinterpret_cast<uint32_t *>(p.out + out * D + ch + j) =
+                            pack_bf16(y[j] * inv, y[j + 1] * inv);
+                    if (p.lse && ch == 0)
+                        p.lse[out] = sum > 0.0f ? (m4 + __builtin_amdgcn_logf(sum)) * kLn2
+                                                : -__builtin_inff();
+                }
+            } else {
+                const int64_t part = (int64_t)split * p.S * p.q_heads + out;
+#pragma unroll
+                for (int j = 0; j < C; j += 4)
+                    *reinterpret_cast<float4 *>(p.part_o + part * D + ch + j) =
+                        make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                if (ch == 0) p.part_ml[part] = make_float2(m4, sum);
+            }
+        }
+    }
+}
+
+// One wave joins the parts of one (row, head): the weights of up to 64 parts a
+// lane each, then the parts in order.  Reads what the blocks wrote, once.
+template <int D, bool SEL>
+__global__ __launch_bounds__(256) void join_kernel(KvAttendParams p)
+{
+    constexpr int C = D / 64;
+    const KvCache &kc = p.c;
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    if (unit >= p.S * p.q_heads) return;
+    const int64_t row = unit / p.q_heads;
+    int own;
+    const int seq = find_seq(kc.cu, kc.nseq, row, 1, 0);
+    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
+    if (row < c0 || row >= c1) return;
+    if constexpr (SEL) {
+        own = clamped(p.valid_len[row], p.W);
+    } else {
+        const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+        const int64_t x = p.causal ? (int64_t)len - (c1 - c0) + (row - c0) + 1 : len;
+        own = x < 0 ? 0 : (int)x;
+    }
+    if (own <= p.chunk) return;                     // written by its one block
+    int parts = (own + p.chunk - 1) / p.chunk;
+    parts = parts < p.nsplit ? parts : p.nsplit;
+    const int64_t step = p.S * p.q_heads;
+    float m = -__builtin_inff(), l = 0.0f, y[C] = {};
+    for (int s0 = 0; s0 < parts; s0 += 64) {
+        const int k = parts - s0 < 64 ? parts - s0 : 64;
+        float2 ml = make_float2(-__builtin_inff(), 0.0f);
+        if (lane < k) ml = p.part_ml[(s0 + lane) * step + unit];
+        float top = ml.x;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
+        const float m2 = fmaxf(m, top);
+        const float old = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - m2);
+        const float w = ml.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m2);
+        float sum = ml.y * w;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+        l = l * old + sum;
+#pragma unroll
+        for (int j = 0; j < C; ++j) y[j] *= old;
+        m = m2;
+#pragma unroll 4
+        for (int s = 0; s < k; ++s) {
+            const float ws = __shfl(w, s);
+            const float *src = p.part_o + ((s0 + s) * step + unit) * D + lane * C;
+#pragma unroll
+            for (int j = 0; j < C; ++j) y[j] += ws * src[j];
+        }
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if constexpr (C == 2) {
+        *reinterpret_cast<uint32_t *>(p.out + unit * D + lane * 2) = pack_bf16(y[0] * inv, y[1] * inv);
+    } else {
+        const uint32_t x = pack_bf16(y[0] * inv, 0.0f);
+        p.out[unit * D + lane] = (uint16_t)x;
+    }
+    if (p.lse && lane == 0)
+        p.lse[unit] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+}
+
+template <bool FP8, int D>
+hipError_t launch_rows(int nt, const KvAttendParams &p, hipStream_t st)
+{
+    const int ngrp = (p.group + kKvHeadTile - 1) / kKvHeadTile;
+    const dim3 g((uint32_t)(p.slots * p.nsplit * ngrp * p.c.heads)), b(256);
+    const bool sel = p.idx != nullptr;
+#define ROWS(NT)                                                     \
+    case NT:                                                         \
+        if (sel) rows_kernel<FP8, D, NT, true><<<g, b, 0, st>>>(p);  \
+        else rows_kernel<FP8, D, NT, false><<<g, b, 0, st>>>(p);     \
+        break
+    switch (nt) {
+        ROWS(1);
+        ROWS(2);
+        ROWS(3);
+        ROWS(4);
+    default: return hipErrorInvalidValue;
+    }
+#undef ROWS
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hipStream_t st)
+{
+    const bool fp8 = dtype == 2;
+    if (d == 64) return fp8 ? launch_rows<true, 64>(nt, p, st) : launch_rows<false, 64>(nt, p, st);
+    if (d == 128) return fp8 ? launch_rows<true, 128>(nt, p, st) : launch_rows<false, 128>(nt, p, st);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st)
+{
+    const dim3 g((uint32_t)((p.S * p.q_heads + 3) / 4)), b(256);
+    const bool sel = p.idx != nullptr;
+    if (d == 64) {
+        if (sel) join_kernel<64, true><<<g, b, 0, st>>>(p);
+        else join_kernel<64, false><<<g, b, 0, st>>>(p);
+    } else {
+        if (sel) join_kernel<128, true><<<g, b, 0, st>>>(p);
+        else join_kernel<128, false><<<g, b, 0, st>>>(p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace dsai

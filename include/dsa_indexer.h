@@ -399,6 +399,164 @@ int indexer_screen_certificates(indexer_t h, const void *q, const float *q_scale
                                 float *weights, float *bound_weights, float *knorm_coef,
                                 float *aggregate, int32_t *activations, void *stream);
 
+/*
+ * ---- Paged key/value cache ------------------------------------------------
+ *
+ * The selection's consumer: keys and values of the attention layers in pages,
+ * the appending of new tokens, and attention over all of a sequence's tokens
+ * or over the positions that indexer_score_topk selected.
+ *
+ * indexer_kv_cache describes the buffers (host struct, read during the call):
+ *   dtype     IDX_BF16 or IDX_FP8_E4M3 (IDX_F32: IDX_EUNSUPPORTED).
+ *   device    the GPU that all device pointers of the call belong to.
+ *   heads, d  key/value heads and their channels; d is 64 or 128.
+ *   page      tokens per page: 16, 32, 64 or 128.
+ *   pages     pages in the buffers; pages * heads * page < 2^32 - page * heads.
+ *   k, v      device, [pages, heads, page, d] of dtype, 16-byte aligned.
+ *   k_scale, v_scale  device fp32 [pages, heads], the scale of each page and
+ *             head (value = code * scale; positive); NULL for IDX_BF16.
+ *
+ * indexer_kv_seqs describes the sequences of one call:
+ *   cu_q      device int32 [nseq + 1]: the call's rows of sequence i are
+ *             [cu_q[i], cu_q[i+1]); ascending, cu_q[0] = 0, cu_q[nseq] <= the
+ *             row count.  Rows from cu_q[nseq] on belong to no sequence:
+ *             nothing is written for them.
+ *   seq_len   device int32 [nseq]: tokens that the cache holds of sequence i.
+ *   table     device int32, page ids of sequence i at table + i *
+ *             table_stride, entry j for positions [j * page, (j + 1) * page);
+ *             entries past the sequence's last page may hold anything.
+ *   table_width  entries that may be read of a row (table_width * page <
+ *             2^31); seq_len above table_width * page is taken as that.
+ *   nseq      sequences (0 is valid: nothing is done).
+ * The arrays are read on the device only.  Whatever they hold, every access
+ * stays in bounds: offsets and lengths are clamped, a position whose page id
+ * is not in [0, pages) is neither written nor read (attention takes it as
+ * masked).  Results for arrays that do not ascend are unspecified.
+ *
+ * indexer_kv_rows is a tensor [rows, heads, d] of bf16 with strides in
+ * elements between rows and between heads; ptr is 16-byte aligned and both
+ * strides are multiples of 8 and not negative (IDX_EINVAL).
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, keep nothing
+ * between calls and can be captured into a graph.
+ */
+typedef struct {
+    int dtype, device;
+    int heads, d, page;
+    int64_t pages;
+    void *k, *v;
+    float *k_scale, *v_scale;
+} indexer_kv_cache;
+
+typedef struct {
+    const int32_t *cu_q, *seq_len, *table;
+    int64_t table_stride;
+    int table_width, nseq;
+} indexer_kv_seqs;
+
+typedef struct {
+    void *ptr;
+    int64_t row_stride, head_stride;
+} indexer_kv_rows;
+
+/*
+ * Append N new tokens: row t of sequence i goes to position seq_len[i] + (t -
+ * cu_q[i]), seq_len holding the lengths before the call (the caller adds the
+ * new tokens to it afterwards).
+ *   k, v      bf16 [N, heads, d].
+ *   cos, sin  device fp32 [rope_rows, rot / 2], contiguous, 16-byte aligned,
+ *             or both NULL (no rotation): channel pair j of the first rot
+ *             channels of a key at position p turns by the angle of row p,
+ *             (a, b) -> (a cos - b sin, b cos + a sin), each product and sum
+ *             rounded to fp32.  rot is a multiple of 16 (IDX_EUNSUPPORTED
+ *             otherwise), at most d.
+ *   interleaved  1: pair j is channels 2j and 2j + 1; 0: j and j + rot / 2.
+ *   q, q_heads, q_out  bf16 [N, q_heads, d]: the new tokens' queries, turned
+ *             the same way into q_out (rounded to nearest even; may be q
+ *             itself, may not overlap it otherwise); q_heads = 0: none.  The
+ *             rows of q_out must not overlap: one of its strides spans the
+ *             whole of the other (IDX_EINVAL).
+ * Positions at or past table_width * page or (with a rotation) rope_rows are
+ * not written, nor are their queries when past rope_rows.
+ * IDX_BF16 rounds to nearest even.  IDX_FP8_E4M3: a page's scale for a head
+ * becomes the smallest power of two s (2^-117 .. 2^120) with amax <= 448 s,
+ * amax the largest finite magnitude of the tokens the call adds to the page --
+ * or stays what it is when that is larger and the page holds tokens of the
+ * sequence already (seq_len[i] not a multiple of page).  When it grows, the
+ * held tokens' codes are brought to the new scale, rounded to nearest even;
+ * codes are x / s rounded likewise.  An infinite or NaN element is stored as
+ * NaN.  Slots behind the appended tokens keep what they hold.
+ * A page must not be written for two sequences in one call.
+ */
+int indexer_kv_append(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs,
+                      const indexer_kv_rows *k, const indexer_kv_rows *v, int64_t N,
+                      const float *cos, const float *sin, int64_t rope_rows, int rot,
+                      int interleaved, const indexer_kv_rows *q, int q_heads,
+                      const indexer_kv_rows *q_out, void *stream);
+
+/*
+ * Attention of S query rows over their sequences' tokens:
+ *     o = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)
+ * The n rows of sequence i are its last n positions (seq_len holding the
+ * lengths after the append): row t sits at position seq_len[i] - n + (t -
+ * cu_q[i]) and, with causal = 1, sees the tokens up to and at its own; with 0
+ * it sees all seq_len[i] of them.
+ *   q         bf16 [S, q_heads, d]; q_heads a multiple of the cache's heads,
+ *             query head h reads key head h / (q_heads / heads).
+ *   scale     factor of the scores, finite.
+ *   max_len   host, an upper bound on seq_len (0 = unknown: table_width *
+ *             page); sizes the split along the keys and the workspace.  A
+ *             longer sequence breaks the precondition: its rows' results are
+ *             unspecified, every access stays in bounds.
+ *   out       device bf16 [S, q_heads, d], contiguous, 16-byte aligned.
+ *   lse       device fp32 [S, q_heads] or NULL.
+ *   workspace device, 16-byte aligned, of at least
+ *             indexer_kv_attend_workspace_bytes(...) bytes for the same sizes
+ *             (NULL when that is 0).  Calls that share one must be ordered.
+ * A row that sees no token gets out = 0 and lse = -inf.  Scores, softmax
+ * statistics and sums are fp32; the probabilities are rounded to bf16 for the
+ * product with the values, the result once more.  Preconditions not checked:
+ * q and the tokens within seq_len finite, scales positive; everything else in
+ * the cache (unused pages, slots past seq_len, their scales) may hold
+ * anything, NaN included.  Results do not depend on timing: the same call
+ * gives the same bits.
+ */
+int indexer_kv_attend(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs,
+                      const indexer_kv_rows *q, int64_t S, int q_heads, float scale, int causal,
+                      int64_t max_len, void *out, float *lse, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of indexer_kv_attend.  Host-only; the pointers in seqs are
+ * not looked at (nseq and the table's sizes are). */
+int indexer_kv_attend_workspace_bytes(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs,
+                                      int64_t S, int q_heads, int64_t max_len, size_t *bytes);
+
+/*
+ * Attention of S query rows over selected positions, as indexer_score_topk
+ * and indexer_score_topk_varlen write them: row t of sequence i attends to
+ * the positions idx[t, j] - idx0[i], j < valid_len[t] (clamped to [0, W]);
+ * entries outside [0, seq_len[i]), -1 among them, are ignored.  In the
+ * sequence's cache a position is whatever the indexer's entries count: tokens
+ * (m = 1, or IDX_EXPAND), or compressed blocks.
+ *   idx       device int32 [S, W], contiguous; any order, a position given
+ *             twice counts twice.
+ *   valid_len device int32 [S].
+ *   idx0      device int32 [nseq] or NULL (0): the entry of each sequence's
+ *             position 0 (cu_k or cu_tok of a varlen call).
+ * There is no causal mask beside the selection.  Everything else is as in
+ * indexer_kv_attend; a row without a valid entry gets out = 0, lse = -inf.
+ */
+int indexer_kv_attend_selected(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs,
+                               const indexer_kv_rows *q, int64_t S, int q_heads, float scale,
+                               const int32_t *idx, int W, const int32_t *valid_len,
+                               const int32_t *idx0, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of indexer_kv_attend_selected.  Host-only, as above. */
+int indexer_kv_attend_selected_workspace_bytes(const indexer_kv_cache *cache,
+                                               const indexer_kv_seqs *seqs, int64_t S, int q_heads,
+                                               int W, size_t *bytes);
+
 /* Static text for a status code, followed (for IDX_EHIP) by the calling
  * thread's last HIP error.  Never NULL. */
 const char *indexer_strerror(int code);
