@@ -41,7 +41,8 @@ struct KvAttendParams {
     int64_t q_tok, q_head;
     int64_t S;
     int q_heads, group;       // query heads in all, and per key head
-    float c2;                 // softmax scale * log2(e)
+    float c2;                 // |softmax scale| * log2(e), or 1 where that is 0
+    uint32_t q_and, q_xor;    // the scale's sign, or its being 0, on pairs of query elements
     int causal;
     uint16_t *out;            // [S, q_heads, d] bf16
     float *lse;               // [S, q_heads] or null
@@ -63,8 +64,11 @@ hipError_t launch_kv_append(int dtype, int d, const KvAppendParams &p, hipStream
 
 // mt: 16-column tiles of query rows x heads per block (1..4)
 hipError_t launch_kv_rows(int dtype, int d, int mt, const KvAttendParams &p, hipStream_t st);
+// 256 columns per block: many query rows
+hipError_t launch_kv_tiles(int dtype, int d, const KvAttendParams &p, hipStream_t st);
 hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st);
 
+constexpr int kKvTileCols = 256;  // columns of a launch_kv_tiles block
 constexpr int kKvHeadTile = 64;   // query heads of one key head that a block takes at most
 
 }  // namespace dsai

@@ -102,12 +102,15 @@ dsai::KvCache kernel_cache(const indexer_kv_cache *c, const indexer_kv_seqs *s)
 // How a call is cut into blocks; depends on host sizes only, so that the
 // workspace functions and the calls agree.
 struct Plan {
+    bool tiles;
     int nt, tile_rows, nsplit, chunk;
     int64_t slots, part_ml, bytes;
 };
 
 constexpr int64_t kFillBlocks = 512;  // two blocks for each CU
 constexpr int64_t kMinChunk = 256;    // keys that are worth a block of four waves
+constexpr int64_t kFillTiles = 256;   // blocks of eight waves, one for each CU
+constexpr int64_t kMinTileChunk = 512;
 
 Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int64_t max_len,
                bool selected)
@@ -116,15 +119,18 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
     const int group = q_heads / c->heads, gsize = std::min(group, dsai::kKvHeadTile);
     const int64_t ngrp = div_up(group, dsai::kKvHeadTile);
     const int64_t rows = selected ? 1 : div_up(S, std::max(nseq, 1));  // of a sequence, on average
-    const int64_t cols = std::min<int64_t>(std::max<int64_t>(1, dsai::kKvHeadTile / gsize),
-                                           std::max<int64_t>(rows, 1)) * gsize;
-    p.nt = (int)div_up(cols, 16);
-    p.tile_rows = selected ? 1 : std::max(1, 16 * p.nt / gsize);
+    p.tiles = rows * gsize > dsai::kKvHeadTile;
+    if (p.tiles) {
+        p.tile_rows = dsai::kKvTileCols / gsize;
+    } else {
+        p.nt = (int)div_up(rows * gsize, 16);
+        p.tile_rows = selected ? 1 : 16 * p.nt / gsize;
+    }
     p.slots = selected ? S : S / p.tile_rows + nseq;
-    const int64_t units = std::max<int64_t>(1, selected ? S : std::max<int64_t>(S / p.tile_rows, 1)) *
-                          c->heads * ngrp;
-    const int64_t want = std::max<int64_t>(1, kFillBlocks / units);
-    int64_t chunk = std::max(kMinChunk, round_up(div_up(std::max<int64_t>(max_len, 1), want), 128));
+    const int64_t units = std::max<int64_t>(1, S / p.tile_rows) * c->heads * ngrp;
+    const int64_t want = std::max<int64_t>(1, (p.tiles ? kFillTiles : kFillBlocks) / units);
+    int64_t chunk = std::max(p.tiles ? kMinTileChunk : kMinChunk,
+                             round_up(div_up(std::max<int64_t>(max_len, 1), want), 128));
     int64_t nsplit = div_up(std::max<int64_t>(max_len, 1), chunk);
     if (nsplit <= 1) nsplit = 1, chunk = INT32_MAX;
     p.nsplit = (int)nsplit;
@@ -183,7 +189,10 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     p.S = S;
     p.q_heads = q_heads;
     p.group = q_heads / c->heads;
-    p.c2 = (float)((double)scale * 1.4426950408889634074);
+    p.c2 = (float)(std::fabs((double)scale) * 1.4426950408889634074);
+    p.q_and = 0xffffffffu;
+    p.q_xor = scale < 0.0f ? 0x80008000u : 0;
+    if (p.c2 == 0.0f) p.c2 = 1.0f, p.q_and = 0;
     p.causal = causal;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
@@ -198,7 +207,8 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + pl.part_ml);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = dsai::launch_kv_rows(c->dtype, c->d, pl.nt, p, st);
+    hipError_t e = pl.tiles ? dsai::launch_kv_tiles(c->dtype, c->d, p, st)
+                            : dsai::launch_kv_rows(c->dtype, c->d, pl.nt, p, st);
     if (e != hipSuccess) return fail_hip(e);
     if (pl.nsplit > 1) {
         e = dsai::launch_kv_join(c->d, p, st);

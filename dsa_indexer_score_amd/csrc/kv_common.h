@@ -23,6 +23,14 @@ __device__ inline uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// Eight query elements with their sign turned, or cleared: a factor of the
+// scores that is not positive is applied here, so that the kernels' is.
+__device__ inline uint4 signed_queries(uint4 x, uint32_t keep, uint32_t flip)
+{
+    return make_uint4((x.x & keep) ^ flip, (x.y & keep) ^ flip, (x.z & keep) ^ flip,
+                      (x.w & keep) ^ flip);
+}
+
 __device__ inline int clamped(int x, int64_t hi)
 {
     return x < 0 ? 0 : (int64_t)x > hi ? (int)hi : x;

@@ -217,6 +217,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
             const int at = FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
             uint4 x = make_uint4(0, 0, 0, 0);
             if (in) x = *reinterpret_cast<const uint4 *>(src + at);
+            x = signed_queries(x, p.q_and, p.q_xor);
             q[t][s] = __builtin_bit_cast(kvb8, x);
         }
     }

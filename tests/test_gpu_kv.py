@@ -30,7 +30,7 @@ def log(*a):
 class Problem:
     """A filled cache with pages in a shuffled order, NaN wherever no token lies."""
 
-    def __init__(self, seed, dtype, heads, d, page, lens, spare=2, nan=True):
+    def __init__(self, seed, dtype, heads, d, page, lens, spare=2, nan=True, pow2=False):
         g = np.random.default_rng(seed)
         self.g, self.dtype, self.heads, self.d, self.page = g, dtype, heads, d, page
         need = [-(-n // page) for n in lens]
@@ -55,7 +55,7 @@ class Problem:
                 s = np.stack([[okv.pow2_scale(np.abs(x[p, h]).max()) for h in range(heads)]
                               for p in range(pages)]).astype(np.float32)
                 # scales need not be powers of two for attention
-                s = s * np.float32(1.25)
+                s = s * np.float32(1.0 if pow2 else 1.25)
                 c = okv.to_e4m3(x / s[:, :, None, None])
                 if nan:
                     c = np.where(used[:, None, :, None], c, np.uint8(0x7f))
@@ -123,13 +123,22 @@ ATTEND = [
     (BF16, 64, 32, 2, 4, [5000, 257, 0, 3001], [1, 1, 1, 1], True, 1),
     (FP8, 128, 16, 2, 6, [4097, 600], [3, 2], True, 0),
     (FP8, 128, 64, 1, 40, [2500, 1100], [2, 4], True, 0),
+    # many rows: 256 columns a block
+    (FP8, 128, 64, 1, 8, [700], [300], True, 1),
+    (FP8, 64, 16, 2, 3, [1, 400, 0, 333], [1, 400, 5, 100], True, 2),
+    (BF16, 128, 16, 1, 7, [777, 64], [130, 64], True, 0),
+    (BF16, 64, 128, 2, 1, [1000], [600], True, 0),
+    (FP8, 128, 32, 1, 100, [150], [9], True, 0),
+    (FP8, 128, 128, 1, 4, [5000, 90], [70, 70], True, 3),       # split along the keys
+    (BF16, 64, 32, 1, 16, [4500], [33], False, 0),
+    (FP8, 64, 64, 1, 64, [200, 3000], [3, 5], True, 0),
 ]
 
 
-def run_attend(c, nan=True, **kw):
+def run_attend(c, nan=True, pow2=False, **kw):
     dtype, d, page, heads, group, lens, rows, causal, pad = c
     pr = Problem(hash((d, page, heads, group, len(lens), lens[0])) % 1000, dtype, heads, d, page,
-                 lens, nan=nan)
+                 lens, nan=nan, pow2=pow2)
     S = sum(rows) + pad
     cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
     q = pr.queries(S, heads * group)
@@ -145,10 +154,25 @@ def run_attend(c, nan=True, **kw):
     return out, lse, ref, d
 
 
+@pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("c", ATTEND, ids=range(len(ATTEND)))
-def test_attend_matches_the_reference(c):
+def test_attend_matches_the_reference(c, pow2):
     log(c)
-    check(*run_attend(c), where=str(c))
+    check(*run_attend(c, pow2=pow2), where=str(c))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09])
+@pytest.mark.parametrize("c", [ATTEND[5], ATTEND[18], ATTEND[20]], ids=["rows", "fp8", "bf16"])
+def test_attend_with_a_factor_that_is_not_positive(c, scale):
+    dtype, d, page, heads, group, lens, rows, causal, pad = c
+    pr = Problem(11, dtype, heads, d, page, lens)
+    cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    q = pr.queries(sum(rows), heads * group)
+    ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
+                     pr.cache["v"], pr.scale["v"], scale)
+    out, lse = pr.gpu().attend(q.to(DEV), dev(cu), dev(pr.lens), dev(pr.table), scale=scale,
+                               with_lse=True)
+    check(out, lse, ref, d, str(scale))
 
 
 @pytest.mark.parametrize("c", [ATTEND[0], ATTEND[14], ATTEND[15]], ids=["short", "long", "ragged"])
@@ -175,15 +199,16 @@ def test_attend_reads_strided_queries():
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("group", [4, 64])
 @pytest.mark.parametrize("dtype", [FP8, BF16])
-def test_pages_that_do_not_exist_are_masked(dtype):
+def test_pages_that_do_not_exist_are_masked(dtype, group):
     pr = Problem(5, dtype, 2, 64, 16, [100, 60, 3000])
     pr.table[0, 2] = -1
     pr.table[1, 0] = 10 ** 9
     pr.table[1, 1:4] = np.iinfo(np.int32).min
     pr.table[2, 7:150] = 77777
     cu = np.array([0, 3, 5, 6], np.int32)
-    q = pr.queries(6, 8)
+    q = pr.queries(6, 2 * group)
     ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
                      pr.cache["v"], pr.scale["v"], 64 ** -0.5)
     out, lse = pr.gpu().attend(q.to(DEV), dev(cu), dev(pr.lens), dev(pr.table), with_lse=True)
