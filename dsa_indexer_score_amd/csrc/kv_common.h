@@ -5,6 +5,8 @@
 
 #include "kv.h"
 
+#define KV_INLINE __attribute__((always_inline))
+
 namespace dsai {
 namespace {
 
@@ -13,6 +15,47 @@ typedef __bf16 kvb2 __attribute__((ext_vector_type(2)));
 typedef float kvf4 __attribute__((ext_vector_type(4)));
 
 __device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The largest of the four lanes n, n + 16, n + 32, n + 48.
+__device__ inline float max_over_rows(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t y = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+    auto b = __builtin_amdgcn_permlane16_swap(y, y, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// The larger of the lanes n and n + 32.
+__device__ inline float max_over_halves(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+
+// What a block of an attention launch works on; blocks of one (slot, split)
+// are neighbours over the heads, so that with eight key heads each XCD (blocks
+// are dealt to them in turn) keeps to one head's keys.
+struct BlockAt {
+    int head, grp, split;
+    int64_t slot;
+};
+
+__device__ inline BlockAt block_at(const KvAttendParams &p)
+{
+    BlockAt r;
+    uint32_t b = blockIdx.x;             // fewer than 2^31 blocks, checked on the host
+    const uint32_t heads = (uint32_t)p.c.heads, slots = (uint32_t)p.slots;
+    const uint32_t ngrp = (uint32_t)(p.group + kKvHeadTile - 1) / kKvHeadTile;
+    r.head = (int)(b % heads);
+    b /= heads;
+    r.grp = (int)(b % ngrp);
+    b /= ngrp;
+    r.split = (int)(b / slots);
+    r.slot = b % slots;
+    return r;
+}
 
 // Two floats to packed bf16, round to nearest even.
 __device__ inline uint32_t pack_bf16(float a, float b)

@@ -34,7 +34,8 @@ namespace dsai {
 namespace {
 
 constexpr int kList = 1024;             // keys resolved to rows at a time
-constexpr uint32_t kNoRow = 0xffffffffu;
+constexpr uint32_t kNoPage = 0xffffffffu;
+constexpr float kSlack = 8.0f;          // log2 of the largest probability against the running maximum
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int N> struct Words;          // N dwords that one load brings
@@ -74,23 +75,18 @@ template <bool FP8, int D> struct Tile {
     uint4 k[2][KU];
     VT v[8];
 
-    __device__ void load(const char *kb, const char *vb, const uint32_t *list, int m, int g)
+    // off: byte offsets of the tile's rows in the cache
+    __device__ void load(const char *kb, const char *vb, const uint64_t *off, int m, int g)
     {
-        constexpr uint32_t RB = D * ES;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t row = list[16 * t + m];
-            const uint4 *p = reinterpret_cast<const uint4 *>(
-                kb + (uint64_t)(row == kNoRow ? 0 : row) * RB) + g;
+            const uint4 *p = reinterpret_cast<const uint4 *>(kb + off[16 * t + m]);
 #pragma unroll
             for (int u = 0; u < KU; ++u) k[t][u] = p[4 * u];
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t row = list[16 * (j >> 2) + 4 * g + (j & 3)];
-            v[j] = *reinterpret_cast<const VT *>(vb + (uint64_t)(row == kNoRow ? 0 : row) * RB +
-                                                 m * (VW * 4));
-        }
+        for (int j = 0; j < 8; ++j)
+            v[j] = *reinterpret_cast<const VT *>(vb + off[16 * (j >> 2) + 4 * g + (j & 3)]);
     }
 
     __device__ kvb8 key(int t, int step) const
@@ -149,9 +145,13 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
     using TL = Tile<FP8, D>;
     constexpr int MT = TL::MT, CH = FP8 ? 4 : 2;  // channels that one dword of values holds
     constexpr int PITCH = D + 4;
-    struct List { uint32_t row[kList]; float ks[FP8 ? kList : 4], vs[FP8 ? kList : 4]; };
+    struct List {
+        uint64_t off[kList];            // byte offsets of the keys' rows
+        float ks[FP8 ? kList : 4], vs[FP8 ? kList : 4];
+        uint32_t bad[kList / 32];       // which of a tile's keys are not there
+    };
     struct Join { float o[4][16][PITCH]; };
-    __shared__ union { List list; Join join; } sm;
+    __shared__ __align__(16) union { List list; Join join; } sm;
     __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
 
     const KvCache &kc = p.c;
@@ -159,15 +159,10 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
     const int n = lane & 15, g = lane >> 4;
 
     // ---- which rows, key head, query heads and keys
-    int64_t b = blockIdx.x;
-    const int head = (int)(b % kc.heads);
-    b /= kc.heads;
     const int gsize = p.group < kKvHeadTile ? p.group : kKvHeadTile;
-    const int ngrp = (p.group + kKvHeadTile - 1) / kKvHeadTile;
-    const int grp = (int)(b % ngrp);
-    b /= ngrp;
-    const int64_t slot = b % p.slots;
-    const int split = (int)(b / p.slots);
+    const BlockAt blk = block_at(p);
+    const int head = blk.head, grp = blk.grp, split = blk.split;
+    const int64_t slot = blk.slot;
 
     const int R = SEL ? 1 : p.tile_rows;
     const int seq = SEL ? find_seq(kc.cu, kc.nseq, slot, 1, 0) : find_seq(kc.cu, kc.nseq, slot, R, 1);
@@ -194,13 +189,11 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
     // ---- the columns: query rows x heads
     kvb8 q[NT][TL::KS];
     int lim[NT];                 // keys that the column sees
-    int64_t orow[NT];            // its output row, or -1
     int minlim = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int col = 16 * t + n, tok = col / gsize, hh = grp * kKvHeadTile + col % gsize;
         const bool in = tok < ntok && hh < p.group;
-        orow[t] = in ? (row0 + tok) * p.q_heads + head * p.group + hh : -1;
         lim[t] = 0x7fffffff;
         if constexpr (!SEL) {
             if (in && p.causal) {
@@ -238,114 +231,148 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
         for (int i = 0; i < MT; ++i) o[t][i] = kvf4{0, 0, 0, 0};
     }
 
-    const char *kb = static_cast<const char *>(kc.k), *vb = static_cast<const char *>(kc.v);
+    // a lane's part of a row: 16-byte chunks of a key from chunk g on, the D / 16
+    // channels of a value from D / 16 n on
+    const char *kb = static_cast<const char *>(kc.k) + g * 16;
+    const char *vb = static_cast<const char *>(kc.v) + n * (TL::VW * 4);
     const int page_mask = (1 << kc.page_shift) - 1;
     const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
+
+    // One tile of 32 keys, s0 + at .. s0 + at + 31 of the entries.
+    auto process = [&](TL &cur, int s0, int at) KV_INLINE {
+        const uint32_t bad = (uint32_t)uniform((int)sm.list.bad[at >> 5]);
+        const bool edge = !SEL && s0 + at + 32 > minlim;
+        float ks[8], vs[8];
+        if constexpr (FP8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 a = *reinterpret_cast<const float4 *>(&sm.list.ks[at + 16 * h + 4 * g]);
+                const float4 b = *reinterpret_cast<const float4 *>(&sm.list.vs[at + 16 * h + 4 * g]);
+                ks[4 * h] = a.x; ks[4 * h + 1] = a.y; ks[4 * h + 2] = a.z; ks[4 * h + 3] = a.w;
+                vs[4 * h] = b.x; vs[4 * h + 1] = b.y; vs[4 * h + 2] = b.z; vs[4 * h + 3] = b.w;
+            }
+        }
+        // keys that are not there: no score (below), and values that cannot be NaN
+        if (bad) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (bad >> (16 * (j >> 2) + 4 * g + (j & 3)) & 1) clear(cur.v[j]);
+        }
+        uint4 pk[NT];
+        kvf4 acc[NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < TL::KS; ++s) {
+                const kvb8 a = cur.key(h, s);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    acc[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        a, q[t][s], s ? acc[t][h] : kvf4{0, 0, 0, 0}, 0, 0, 0);
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if constexpr (NT == 4) __builtin_amdgcn_sched_barrier(0);
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = acc[t][j >> 2][j & 3] * (FP8 ? ks[j] : p.c2);
+            if (bad || edge) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int key = 16 * (j >> 2) + 4 * g + (j & 3);
+                    if ((bad >> key & 1) || s0 + at + key >= lim[t]) x[j] = -__builtin_inff();
+                }
+            }
+            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                              fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            top = max_over_rows(top);
+            if (__ballot(top > mx[t] + kSlack)) {  // also the first tile: mx = -inf
+                const float m2 = fmaxf(mx[t], top);
+                const float a = mx[t] == m2 ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - m2);
+                mx[t] = m2;
+                l[t] *= a;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) o[t][i] *= a;
+            }
+            const float m1 = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = __builtin_amdgcn_exp2f(x[j] - m1);
+                l[t] += x[j];
+                if constexpr (FP8) x[j] *= vs[j];
+            }
+            pk[t] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                               pack_bf16(x[6], x[7]));
+        }
+        if constexpr (NT == 4) __builtin_amdgcn_sched_barrier(0);  // registers are short
+#pragma unroll
+        for (int w = 0; w < TL::VW; ++w) {
+            kvb8 a[CH];
+            cur.values(w, a);
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    o[t][CH * w + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        a[i], __builtin_bit_cast(kvb8, pk[t]), o[t][CH * w + i], 0, 0, 0);
+        }
+    };
 
     for (int s0 = e0; s0 < e1; s0 += kList) {
         // ---- resolve up to kList entries to cache rows and their scales
         const int cnt = e1 - s0 < kList ? e1 - s0 : kList;
         const int padded = (cnt + 31) & ~31;
         if (s0 > e0) __syncthreads();
-        for (int i = tid; i < padded; i += 256) {
-            uint32_t row = kNoRow;
-            float ks = 0.0f, vs = 0.0f;
-            if (i < cnt) {
-                int64_t pos = s0 + i;
-                if constexpr (SEL) pos = (int64_t)p.idx[row0 * p.W + pos] - base;
-                if (!SEL || (pos >= 0 && pos < len)) {
-                    const uint32_t id = (uint32_t)table[pos >> kc.page_shift];
-                    if (id < kc.pages) {
-                        const uint32_t unit = id * (uint32_t)kc.heads + head;
-                        row = (unit << kc.page_shift) + ((int)pos & page_mask);
-                        if constexpr (FP8) {
-                            ks = kc.k_scale[unit] * p.c2;
-                            vs = kc.v_scale[unit];
-                        }
-                    }
+        int64_t pos[kList / 256];
+        uint32_t id[kList / 256];
+        bool there[kList / 256];
+#pragma unroll
+        for (int k = 0; k < kList / 256; ++k) {
+            const int i = tid + 256 * k;
+            there[k] = i < cnt;
+            pos[k] = s0 + i;
+            if constexpr (SEL) {
+                pos[k] = (int64_t)(there[k] ? p.idx[row0 * p.W + pos[k]] : -1) - base;
+                there[k] = there[k] && pos[k] >= 0 && pos[k] < len;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kList / 256; ++k)
+            id[k] = there[k] ? (uint32_t)table[pos[k] >> kc.page_shift] : kNoPage;
+#pragma unroll
+        for (int k = 0; k < kList / 256; ++k) {
+            const int i = tid + 256 * k;
+            there[k] = id[k] < kc.pages;
+            const uint32_t unit = there[k] ? id[k] * (uint32_t)kc.heads + head : 0;
+            const uint64_t row = ((uint64_t)unit << kc.page_shift) +
+                                 (there[k] ? (int)pos[k] & page_mask : 0);
+            if (i < padded) {
+                sm.list.off[i] = row * (uint64_t)(D * TL::ES);
+                if constexpr (FP8) {
+                    sm.list.ks[i] = there[k] ? kc.k_scale[unit] * p.c2 : 0.0f;
+                    sm.list.vs[i] = there[k] ? kc.v_scale[unit] : 0.0f;
                 }
             }
-            sm.list.row[i] = row;
-            if constexpr (FP8) {
-                sm.list.ks[i] = ks;
-                sm.list.vs[i] = vs;
+            const uint64_t bad = __ballot(!there[k]);
+            if (lane == 0) {
+                sm.list.bad[i >> 5] = (uint32_t)bad;
+                sm.list.bad[(i >> 5) + 1] = (uint32_t)(bad >> 32);
             }
         }
         __syncthreads();
 
         // ---- tiles of 32 keys, in turn over the waves, the next one's loads ahead
-        TL cur, nxt;
+        TL a, b;
         int at = wave * 32;
-        if (at < padded) cur.load(kb, vb, sm.list.row + at, n, g);
-        for (; at < padded; at += 128) {
-            if (at + 128 < padded) nxt.load(kb, vb, sm.list.row + at + 128, n, g);
-            // keys that are not there: no score, and values that cannot be NaN
-            const uint32_t *list = sm.list.row + at;
-            const bool gaps = __ballot(list[n] == kNoRow || list[16 + n] == kNoRow) != 0;
-            if (gaps) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (list[16 * (j >> 2) + 4 * g + (j & 3)] == kNoRow) clear(cur.v[j]);
-            }
-            const bool edge = !SEL && s0 + at + 32 > minlim;
-            uint4 pk[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float x[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    kvf4 acc = {0, 0, 0, 0};
-#pragma unroll
-                    for (int s = 0; s < TL::KS; ++s)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cur.key(h, s), q[t][s], acc,
-                                                                      0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = 16 * h + 4 * g + i;
-                        x[4 * h + i] = acc[i] * (FP8 ? sm.list.ks[at + key] : p.c2);
-                        if (gaps && list[key] == kNoRow) x[4 * h + i] = -__builtin_inff();
-                        if (edge && s0 + at + key >= lim[t]) x[4 * h + i] = -__builtin_inff();
-                    }
-                }
-                float top = x[0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                if (__ballot(top > mx[t])) {
-                    const float m2 = fmaxf(mx[t], top);
-                    const float a = mx[t] == m2 ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - m2);
-                    mx[t] = m2;
-                    l[t] *= a;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) o[t][i] *= a;
-                }
-                const float m1 = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = __builtin_amdgcn_exp2f(x[i] - m1);
-                    l[t] += x[i];
-                }
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] *= sm.list.vs[at + 16 * (i >> 2) + 4 * g + (i & 3)];
-                }
-                pk[t] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                   pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            }
-#pragma unroll
-            for (int w = 0; w < TL::VW; ++w) {
-                kvb8 a[CH];
-                cur.values(w, a);
-#pragma unroll
-                for (int i = 0; i < CH; ++i)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        o[t][CH * w + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            a[i], __builtin_bit_cast(kvb8, pk[t]), o[t][CH * w + i], 0, 0, 0);
-            }
-            cur = nxt;
+        if (at < padded) a.load(kb, vb, sm.list.off + at, n, g);
+        while (at < padded) {
+            if (at + 128 < padded) b.load(kb, vb, sm.list.off + at + 128, n, g);
+            process(a, s0, at);
+            at += 128;
+            if (at >= padded) break;
+            if (at + 128 < padded) a.load(kb, vb, sm.list.off + at + 128, n, g);
+            process(b, s0, at);
+            at += 128;
         }
     }
 

@@ -28,8 +28,6 @@
 
 #include "kv_common.h"
 
-#define KV_INLINE __attribute__((always_inline))
-
 namespace dsai {
 namespace {
 
@@ -57,7 +55,7 @@ __device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel)
 }
 
 template <bool FP8, int D>
-__global__ __launch_bounds__(512, 1) void tiles_kernel(KvAttendParams p)
+__global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendParams p)
 {
     constexpr int ES = FP8 ? 1 : 2;
     constexpr int KS = D / 16;          // contraction steps of S
@@ -77,15 +75,10 @@ __global__ __launch_bounds__(512, 1) void tiles_kernel(KvAttendParams p)
     const int st = tid & 255;           // thread of the group
 
     // ---- which rows, key head, query heads and keys
-    int64_t b = blockIdx.x;
-    const int head = (int)(b % kc.heads);
-    b /= kc.heads;
     const int gsize = p.group < kKvHeadTile ? p.group : kKvHeadTile;
-    const int ngrp = (p.group + kKvHeadTile - 1) / kKvHeadTile;
-    const int grp = (int)(b % ngrp);
-    b /= ngrp;
-    const int split = (int)(b / p.slots);
-    const int64_t slot = p.slots - 1 - b % p.slots;   // causal: the longest rows first
+    const BlockAt blk = block_at(p);
+    const int head = blk.head, grp = blk.grp, split = blk.split;
+    const int64_t slot = p.slots - 1 - blk.slot;      // causal: the longest rows first
     const int R = p.tile_rows;
     const int seq = find_seq(kc.cu, kc.nseq, slot, R, 1);
     const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
@@ -334,7 +327,7 @@ __global__ __launch_bounds__(512, 1) void tiles_kernel(KvAttendParams p)
             for (int j = 1; j < 8; ++j) m = fmaxf(m, s[x >> 1][8 * (x & 1) + j]);
             top = fmaxf(top, m * ks[x]);
         }
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = max_over_halves(top);
         if (__ballot(top > mx + kSlack)) {   // also the first tile: mx = -inf
             const float m2 = fmaxf(mx, top);
             const float a = mx == m2 ? 1.0f : __builtin_amdgcn_exp2f(mx - m2);
