@@ -53,6 +53,7 @@ struct KvAttendParams {
     const int32_t *idx0;      // [nseq] or null, subtracted from the entries
     // the split: `chunk` keys a block, nsplit blocks along the keys; rows that
     // need more than one leave (o, m, l) in part_o / part_ml for the join
+    int head_tile, groups;    // query heads of a key head that a block takes, blocks for all
     int tile_rows;            // query rows of a sequence that one block takes
     int64_t slots;            // row tiles, empty ones among them
     int chunk, nsplit;
@@ -62,13 +63,20 @@ struct KvAttendParams {
 
 hipError_t launch_kv_append(int dtype, int d, const KvAppendParams &p, hipStream_t st);
 
-// mt: 16-column tiles of query rows x heads per block (1..4)
-hipError_t launch_kv_rows(int dtype, int d, int mt, const KvAttendParams &p, hipStream_t st);
+// Blocks of a launch: units (slot, split, key head) times groups.
+__host__ __device__ inline int64_t kv_units(const KvAttendParams &p) { return p.slots * p.nsplit * p.c.heads; }
+inline int64_t kv_blocks(const KvAttendParams &p)
+{
+    return p.groups == 1 ? kv_units(p) : (kv_units(p) + 7) / 8 * 8 * p.groups;
+}
+
+// nt: 16-column tiles of query rows x heads per block (1 or 2)
+hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hipStream_t st);
 // 256 columns per block: many query rows
 hipError_t launch_kv_tiles(int dtype, int d, const KvAttendParams &p, hipStream_t st);
 hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st);
 
+constexpr int kKvRowsCols = 32;   // columns of a launch_kv_rows block at most
 constexpr int kKvTileCols = 256;  // columns of a launch_kv_tiles block
-constexpr int kKvHeadTile = 64;   // query heads of one key head that a block takes at most
 
 }  // namespace dsai

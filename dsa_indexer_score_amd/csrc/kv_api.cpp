@@ -103,12 +103,23 @@ dsai::KvCache kernel_cache(const indexer_kv_cache *c, const indexer_kv_seqs *s)
 // workspace functions and the calls agree.
 struct Plan {
     bool tiles;
-    int nt, tile_rows, nsplit, chunk;
+    int nt, head_tile, groups, tile_rows, nsplit, chunk;
     int64_t slots, part_ml, bytes;
 };
 
-constexpr int64_t kFillBlocks = 512;  // two blocks for each CU
-constexpr int64_t kMinChunk = 256;    // keys that are worth a block of four waves
+// Two blocks for each CU: 262,144 keys, 8 key heads, one row take 105 us with
+// 512 blocks, 111 with 768.  A part below 512 keys costs more in the join than
+// it saves (4 rows of 517 keys: 11.3 against 15.7 us a call with parts of 256;
+// 16 rows of 2,048 selected keys 28.4 against 37.5 with parts of 1,024).  64
+// rows of up to 16,384 keys: 258 us with parts of 4,096, 272 with 8,192, 264
+// with 2,048.
+constexpr int64_t kFillBlocks = 512;
+constexpr int64_t kMinChunk = 512;
+constexpr int64_t kRaggedChunk = 4096;
+// Columns (query rows of a sequence x query heads of a key head) up to which a
+// sequence's rows go by blocks of 32 columns, straight from memory.
+constexpr int64_t kFewCols = 64;
+constexpr int kTilesHeads = 64;       // query heads of a key head in a block of 256 columns
 constexpr int64_t kFillTiles = 256;   // blocks of eight waves, one for each CU
 constexpr int64_t kMinTileChunk = 512;
 
@@ -116,22 +127,30 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
                bool selected)
 {
     Plan p{};
-    const int group = q_heads / c->heads, gsize = std::min(group, dsai::kKvHeadTile);
-    const int64_t ngrp = div_up(group, dsai::kKvHeadTile);
+    const int group = q_heads / c->heads;
     const int64_t rows = selected ? 1 : div_up(S, std::max(nseq, 1));  // of a sequence, on average
-    p.tiles = rows * gsize > dsai::kKvHeadTile;
+    p.tiles = !selected && rows * group > kFewCols;
+    const int cols = p.tiles ? dsai::kKvTileCols : dsai::kKvRowsCols;
+    p.head_tile = std::min(group, p.tiles ? kTilesHeads : cols);
+    p.groups = (int)div_up(group, p.head_tile);
     if (p.tiles) {
-        p.tile_rows = dsai::kKvTileCols / gsize;
+        p.tile_rows = cols / p.head_tile;
     } else {
-        p.nt = (int)div_up(rows * gsize, 16);
-        p.tile_rows = selected ? 1 : 16 * p.nt / gsize;
+        p.nt = (int)div_up(std::min<int64_t>(rows * p.head_tile, cols), 16);
+        p.tile_rows = selected ? 1 : 16 * p.nt / p.head_tile;
     }
     p.slots = selected ? S : S / p.tile_rows + nseq;
-    const int64_t units = std::max<int64_t>(1, S / p.tile_rows) * c->heads * ngrp;
-    const int64_t want = std::max<int64_t>(1, (p.tiles ? kFillTiles : kFillBlocks) / units);
-    int64_t chunk = std::max(p.tiles ? kMinTileChunk : kMinChunk,
-                             round_up(div_up(std::max<int64_t>(max_len, 1), want), 128));
-    int64_t nsplit = div_up(std::max<int64_t>(max_len, 1), chunk);
+    const int64_t units = std::max<int64_t>(1, S / p.tile_rows) * c->heads * p.groups;
+    // parts that fill the GPU, as far as they are worth a block each; among
+    // several sequences parts of at most kRaggedChunk keys, so that the longest
+    // does not trail the others
+    const int64_t keys = std::max<int64_t>(max_len, 1);
+    const int64_t fill = (p.tiles ? kFillTiles : kFillBlocks) / units;
+    int64_t nsplit = std::min(fill, keys / (p.tiles ? kMinTileChunk : kMinChunk));
+    if (!p.tiles && !selected && nseq > 1) nsplit = std::max(nsplit, keys / kRaggedChunk);
+    nsplit = std::max<int64_t>(nsplit, 1);
+    int64_t chunk = round_up(div_up(keys, nsplit), 128);
+    nsplit = div_up(keys, chunk);
     if (nsplit <= 1) nsplit = 1, chunk = INT32_MAX;
     p.nsplit = (int)nsplit;
     p.chunk = (int)chunk;
@@ -173,9 +192,7 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     if (!rows_ok(q) || !out || !aligned(out, 16) || !aligned(lse, 4)) return IDX_EINVAL;
     const Plan pl = make_plan(c, S, q_heads, s->nseq, idx ? W : most_keys(c, s, max_len),
                               idx != nullptr);
-    const int64_t blocks = pl.slots * pl.nsplit * c->heads *
-                           div_up(q_heads / c->heads, dsai::kKvHeadTile);
-    if (blocks >= INT32_MAX) return IDX_EUNSUPPORTED;
+    if ((pl.slots * pl.nsplit * c->heads + 8) * pl.groups >= INT32_MAX) return IDX_EUNSUPPORTED;
     if (pl.bytes > 0 && (!workspace || workspace_bytes < (size_t)pl.bytes || !aligned(workspace, 16)))
         return IDX_EWORKSPACE;
 
@@ -200,6 +217,8 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     p.W = W;
     p.valid_len = valid_len;
     p.idx0 = idx0;
+    p.head_tile = pl.head_tile;
+    p.groups = pl.groups;
     p.tile_rows = pl.tile_rows;
     p.slots = pl.slots;
     p.chunk = pl.chunk;

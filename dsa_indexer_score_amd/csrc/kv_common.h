@@ -34,26 +34,33 @@ __device__ inline float max_over_halves(float x)
     return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
-// What a block of an attention launch works on; blocks of one (slot, split)
-// are neighbours over the heads, so that with eight key heads each XCD (blocks
-// are dealt to them in turn) keeps to one head's keys.
+// What a block of an attention launch works on.  Blocks are dealt to the eight
+// XCDs in turn: with eight key heads each XCD keeps to one head's keys, and the
+// groups of one key head's query heads are eight blocks apart, so that the
+// second finds the keys in the L2 that the first filled.
 struct BlockAt {
     int head, grp, split;
     int64_t slot;
+    bool none;
 };
 
 __device__ inline BlockAt block_at(const KvAttendParams &p)
 {
     BlockAt r;
-    uint32_t b = blockIdx.x;             // fewer than 2^31 blocks, checked on the host
+    uint32_t u = blockIdx.x;             // fewer than 2^31 blocks, checked on the host
+    r.grp = 0;
+    r.none = false;
+    if (p.groups > 1) {
+        const uint32_t g = (uint32_t)p.groups, b = u >> 3;
+        r.grp = (int)(b % g);
+        u = (b / g) * 8 + (u & 7);
+        r.none = u >= (uint32_t)kv_units(p);
+    }
     const uint32_t heads = (uint32_t)p.c.heads, slots = (uint32_t)p.slots;
-    const uint32_t ngrp = (uint32_t)(p.group + kKvHeadTile - 1) / kKvHeadTile;
-    r.head = (int)(b % heads);
-    b /= heads;
-    r.grp = (int)(b % ngrp);
-    b /= ngrp;
-    r.split = (int)(b / slots);
-    r.slot = b % slots;
+    r.head = (int)(u % heads);
+    u /= heads;
+    r.split = (int)(u / slots);
+    r.slot = u % slots;
     return r;
 }
 

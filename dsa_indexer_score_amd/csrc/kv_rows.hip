@@ -7,7 +7,7 @@
 // scores are kept in base 2 (scale * log2 e, times the key page's scale, is one
 // fp32 factor on the exact bf16 products that the matrix unit sums in fp32).
 //
-// A block takes the query rows of one key head (up to 64 columns: rows of a
+// A block takes the query rows of one key head (up to 32 columns: rows of a
 // sequence times the head's query heads) and a range of the keys; its four
 // waves take turns at tiles of 32 keys, each with a softmax state of its own,
 // joined through LDS at the end.  Nothing but the list of key rows is shared in
@@ -36,6 +36,7 @@ namespace {
 constexpr int kList = 1024;             // keys resolved to rows at a time
 constexpr uint32_t kNoPage = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 of the largest probability against the running maximum
+constexpr int kFewParts = 16;           // parts that one wave joins
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int N> struct Words;          // N dwords that one load brings
@@ -140,7 +141,7 @@ template <bool FP8, int D> struct Tile {
 };
 
 template <bool FP8, int D, int NT, bool SEL>
-__global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendParams p)
+__global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
 {
     using TL = Tile<FP8, D>;
     constexpr int MT = TL::MT, CH = FP8 ? 4 : 2;  // channels that one dword of values holds
@@ -159,8 +160,9 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
     const int n = lane & 15, g = lane >> 4;
 
     // ---- which rows, key head, query heads and keys
-    const int gsize = p.group < kKvHeadTile ? p.group : kKvHeadTile;
+    const int gsize = p.head_tile;
     const BlockAt blk = block_at(p);
+    if (blk.none) return;
     const int head = blk.head, grp = blk.grp, split = blk.split;
     const int64_t slot = blk.slot;
 
@@ -192,7 +194,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
     int minlim = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int col = 16 * t + n, tok = col / gsize, hh = grp * kKvHeadTile + col % gsize;
+        const int col = 16 * t + n, tok = col / gsize, hh = grp * gsize + col % gsize;
         const bool in = tok < ntok && hh < p.group;
         lim[t] = 0x7fffffff;
         if constexpr (!SEL) {
@@ -272,7 +274,6 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
             }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            if constexpr (NT == 4) __builtin_amdgcn_sched_barrier(0);
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = acc[t][j >> 2][j & 3] * (FP8 ? ks[j] : p.c2);
@@ -304,7 +305,6 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
             pk[t] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                pack_bf16(x[6], x[7]));
         }
-        if constexpr (NT == 4) __builtin_amdgcn_sched_barrier(0);  // registers are short
 #pragma unroll
         for (int w = 0; w < TL::VW; ++w) {
             kvb8 a[CH];
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
         // thread: column tid / 16, D / 16 channels
         constexpr int C = D / 16;
         const int cl = tid >> 4, ch = (tid & 15) * C, col = 16 * t + cl;
-        const int tok = col / gsize, hh = grp * kKvHeadTile + col % gsize;
+        const int tok = col / gsize, hh = grp * gsize + col % gsize;
         if (tok < ntok && hh < p.group) {
             float m4 = sm_m[0][col];
 #pragma unroll
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
             if constexpr (!SEL) {
                 if (p.causal) {
                     const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
-                    own = x < 0 ? 0 : (int)x;
+                    own = x < 0 ? 0 : x < len ? (int)x : len;
                 }
             }
             if (own <= p.chunk) {
@@ -459,74 +459,82 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void rows_kernel(KvAttendPara
     }
 }
 
-// One wave joins the parts of one (row, head): the weights of up to 64 parts a
-// lane each, then the parts in order.  Reads what the blocks wrote, once.
-template <int D, bool SEL>
-__global__ __launch_bounds__(256) void join_kernel(KvAttendParams p)
+// One block joins the parts of one (row, head): D / 4 threads a part, as many
+// parts at a time as T threads hold and those eight deep; each thread adds its
+// parts in order and the threads of a channel are added in order.  Bound by
+// latency: with 256 threads 64 parts are one round of loads (24 -> 5.9 us for 64
+// rows x heads of 64 parts against one wave each), with 64 threads few parts
+// keep fewer waves (4,096 rows x heads of at most 4 parts: 9.2 -> 5.5 us).
+template <int D, bool SEL, int T>
+__global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
 {
-    constexpr int C = D / 64;
+    constexpr int TP = D / 4, NG = T / TP;
+    __shared__ float sm_y[NG][D + 4];
+    __shared__ float sm_m[4], sm_l[NG];
     const KvCache &kc = p.c;
-    const int lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
-    if (unit >= p.S * p.q_heads) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int64_t unit = blockIdx.x;
     const int64_t row = unit / p.q_heads;
-    int own;
     const int seq = find_seq(kc.cu, kc.nseq, row, 1, 0);
     const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
     if (row < c0 || row >= c1) return;
+    int own;
     if constexpr (SEL) {
         own = clamped(p.valid_len[row], p.W);
     } else {
         const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
         const int64_t x = p.causal ? (int64_t)len - (c1 - c0) + (row - c0) + 1 : len;
-        own = x < 0 ? 0 : (int)x;
+        own = x < 0 ? 0 : x < len ? (int)x : len;
     }
     if (own <= p.chunk) return;                     // written by its one block
     int parts = (own + p.chunk - 1) / p.chunk;
     parts = parts < p.nsplit ? parts : p.nsplit;
     const int64_t step = p.S * p.q_heads;
-    float m = -__builtin_inff(), l = 0.0f, y[C] = {};
-    for (int s0 = 0; s0 < parts; s0 += 64) {
-        const int k = parts - s0 < 64 ? parts - s0 : 64;
-        float2 ml = make_float2(-__builtin_inff(), 0.0f);
-        if (lane < k) ml = p.part_ml[(s0 + lane) * step + unit];
-        float top = ml.x;
+    float m = -__builtin_inff();
+    for (int s = tid; s < parts; s += T) m = fmaxf(m, p.part_ml[s * step + unit].x);
 #pragma unroll
-        for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
-        const float m2 = fmaxf(m, top);
-        const float old = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - m2);
-        const float w = ml.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m2);
-        float sum = ml.y * w;
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
-        l = l * old + sum;
-#pragma unroll
-        for (int j = 0; j < C; ++j) y[j] *= old;
-        m = m2;
-#pragma unroll 4
-        for (int s = 0; s < k; ++s) {
-            const float ws = __shfl(w, s);
-            const float *src = p.part_o + ((s0 + s) * step + unit) * D + lane * C;
-#pragma unroll
-            for (int j = 0; j < C; ++j) y[j] += ws * src[j];
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    if constexpr (T > 64) {
+        if (lane == 0) sm_m[wave] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    }
+    const int grp = tid / TP, ch = tid % TP * 4;
+    float l = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (m != -__builtin_inff()) {
+#pragma unroll 8
+        for (int s = grp; s < parts; s += NG) {
+            const float2 ml = p.part_ml[s * step + unit];
+            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + (s * step + unit) * D + ch);
+            const float w = __builtin_amdgcn_exp2f(ml.x - m);
+            l += w * ml.y;
+            y[0] += w * x.x;
+            y[1] += w * x.y;
+            y[2] += w * x.z;
+            y[3] += w * x.w;
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    if constexpr (C == 2) {
-        *reinterpret_cast<uint32_t *>(p.out + unit * D + lane * 2) = pack_bf16(y[0] * inv, y[1] * inv);
-    } else {
-        const uint32_t x = pack_bf16(y[0] * inv, 0.0f);
-        p.out[unit * D + lane] = (uint16_t)x;
+    *reinterpret_cast<float4 *>(&sm_y[grp][ch]) = make_float4(y[0], y[1], y[2], y[3]);
+    if (ch == 0) sm_l[grp] = l;
+    __syncthreads();
+    if (tid >= D / 2) return;
+    float sum = 0.0f, a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        sum += sm_l[g];
+        a += sm_y[g][2 * tid];
+        b += sm_y[g][2 * tid + 1];
     }
-    if (p.lse && lane == 0)
-        p.lse[unit] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    *reinterpret_cast<uint32_t *>(p.out + unit * D + 2 * tid) = pack_bf16(a * inv, b * inv);
+    if (p.lse && tid == 0)
+        p.lse[unit] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_inff();
 }
 
 template <bool FP8, int D>
 hipError_t launch_rows(int nt, const KvAttendParams &p, hipStream_t st)
 {
-    const int ngrp = (p.group + kKvHeadTile - 1) / kKvHeadTile;
-    const dim3 g((uint32_t)(p.slots * p.nsplit * ngrp * p.c.heads)), b(256);
+    const dim3 g((uint32_t)kv_blocks(p)), b(256);
     const bool sel = p.idx != nullptr;
 #define ROWS(NT)                                                     \
     case NT:                                                         \
@@ -536,8 +544,6 @@ hipError_t launch_rows(int nt, const KvAttendParams &p, hipStream_t st)
     switch (nt) {
         ROWS(1);
         ROWS(2);
-        ROWS(3);
-        ROWS(4);
     default: return hipErrorInvalidValue;
     }
 #undef ROWS
@@ -556,15 +562,22 @@ hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hip
 
 hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st)
 {
-    const dim3 g((uint32_t)((p.S * p.q_heads + 3) / 4)), b(256);
+    const dim3 g((uint32_t)(p.S * p.q_heads));
     const bool sel = p.idx != nullptr;
+    if (d != 64 && d != 128) return hipErrorInvalidValue;
+#define JOIN(D, T)                                              \
+    do {                                                        \
+        if (sel) join_kernel<D, true, T><<<g, T, 0, st>>>(p);   \
+        else join_kernel<D, false, T><<<g, T, 0, st>>>(p);      \
+    } while (0)
     if (d == 64) {
-        if (sel) join_kernel<64, true><<<g, b, 0, st>>>(p);
-        else join_kernel<64, false><<<g, b, 0, st>>>(p);
+        if (p.nsplit > kFewParts) JOIN(64, 256);
+        else JOIN(64, 64);
     } else {
-        if (sel) join_kernel<128, true><<<g, b, 0, st>>>(p);
-        else join_kernel<128, false><<<g, b, 0, st>>>(p);
+        if (p.nsplit > kFewParts) JOIN(128, 256);
+        else JOIN(128, 64);
     }
+#undef JOIN
     return hipGetLastError();
 }
 

@@ -75,8 +75,9 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
     const int st = tid & 255;           // thread of the group
 
     // ---- which rows, key head, query heads and keys
-    const int gsize = p.group < kKvHeadTile ? p.group : kKvHeadTile;
+    const int gsize = p.head_tile;
     const BlockAt blk = block_at(p);
+    if (blk.none) return;
     const int head = blk.head, grp = blk.grp, split = blk.split;
     const int64_t slot = p.slots - 1 - blk.slot;      // causal: the longest rows first
     const int R = p.tile_rows;
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
     const int ntile = (e1 - e0 + kTile - 1) / kTile;
 
     // ---- the lane's column
-    const int col = wave * 32 + n, tok = col / gsize, hh = grp * kKvHeadTile + col % gsize;
+    const int col = wave * 32 + n, tok = col / gsize, hh = grp * gsize + col % gsize;
     const bool in = tok < ntok && hh < p.group;
     int own = len;                       // keys that the column sees
     if (p.causal) {
@@ -431,8 +432,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
 
 hipError_t launch_kv_tiles(int dtype, int d, const KvAttendParams &p, hipStream_t st)
 {
-    const int ngrp = (p.group + kKvHeadTile - 1) / kKvHeadTile;
-    const dim3 g((uint32_t)(p.slots * p.nsplit * ngrp * p.c.heads)), b(512);
+    const dim3 g((uint32_t)kv_blocks(p)), b(512);
     const bool fp8 = dtype == 2;
     if (d == 64) {
         if (fp8) tiles_kernel<true, 64><<<g, b, 0, st>>>(p);

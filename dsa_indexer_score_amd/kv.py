@@ -17,6 +17,12 @@ from ._lib import IDX_BF16, IDX_FP8_E4M3
 
 _DTYPE_CODE = {torch.bfloat16: IDX_BF16, torch.float8_e4m3fn: IDX_FP8_E4M3}
 _PAGES = (16, 32, 64, 128)
+_INT32, _BF16 = torch.int32, torch.bfloat16
+
+# The current stream's handle without a Stream object around it: a decode step
+# makes calls that take the GPU a few microseconds, and the object costs two.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -53,7 +59,7 @@ class KVCache:
             if t is not None and (t.device != k.device or not t.is_cuda or not t.is_contiguous()):
                 raise ValueError(f"{name} must be contiguous on the GPU of k")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self._gpu = k.device, k.dtype, k.get_device()
         self.pages, self.heads, self.page, self.d = pages, heads, page, d
         self._lib = _lib.load()
         self._c = _lib.KvCache(_DTYPE_CODE[k.dtype], k.device.index or 0, heads, d, page, pages,
@@ -70,37 +76,43 @@ class KVCache:
             if dtype == torch.float8_e4m3fn else [None, None]
         return cls(k, v, k_scale=s[0], v_scale=s[1])
 
-    # ---- arguments
+    # ---- arguments (get_device() is -1 for tensors that are not on a GPU)
     def _seqs(self, cu, seq_len, table):
-        n = seq_len.numel()
-        if seq_len.dim() != 1 or cu.dim() != 1 or cu.numel() != n + 1 or table.dim() != 2 or \
-                table.shape[0] != n:
+        n, gpu = seq_len.numel(), self._gpu
+        if seq_len.dim() != 1 or cu.dim() != 1 or cu.numel() != n + 1 or table.dim() != 2:
             raise ValueError("cu must be [nseq + 1], seq_len [nseq] and table [nseq, width]")
-        for name, t in (("cu", cu), ("seq_len", seq_len), ("table", table)):
-            if t.dtype != torch.int32 or t.device != self.device:
-                raise ValueError(f"{name} must be int32 on {self.device}")
-        if not (cu.is_contiguous() and seq_len.is_contiguous()) or \
-                (table.shape[1] > 1 and table.stride(1) != 1):
+        rows, width = table.shape
+        stride, inner = table.stride()
+        if rows != n:
+            raise ValueError("cu must be [nseq + 1], seq_len [nseq] and table [nseq, width]")
+        if cu.dtype is not _INT32 or seq_len.dtype is not _INT32 or table.dtype is not _INT32 or \
+                cu.get_device() != gpu or seq_len.get_device() != gpu or table.get_device() != gpu:
+            raise ValueError(f"cu, seq_len and table must be int32 on {self.device}")
+        if not (cu.is_contiguous() and seq_len.is_contiguous()) or (inner != 1 and width > 1):
             raise ValueError("cu and seq_len must be contiguous, and table's rows")
-        width = table.shape[1]
-        stride = table.stride(0) if n > 1 else width
-        if stride < width:
+        if n <= 1:
+            stride = width
+        elif stride < width:
             raise ValueError("table's rows must not overlap")
         return _lib.KvSeqs(cu.data_ptr(), seq_len.data_ptr(), table.data_ptr(), stride, width, n)
 
     def _rows(self, name, t, rows=None, heads=None):
         """A [rows, heads, d] bf16 tensor with strides, as the library takes it."""
-        if t.dtype != torch.bfloat16 or t.device != self.device:
+        if t.dtype is not _BF16 or t.get_device() != self._gpu:
             raise TypeError(f"{name} must be bfloat16 on {self.device}")
-        if t.dim() != 3 or t.shape[2] != self.d or (rows is not None and t.shape[0] != rows) or \
-                (heads is not None and t.shape[1] != heads):
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != self.d or (rows is not None and shape[0] != rows) or \
+                (heads is not None and shape[1] != heads):
             raise ValueError(f"{name} must be [rows, heads, {self.d}]"
                              f"{'' if rows is None else f' with {rows} rows'}"
                              f"{'' if heads is None else f' and {heads} heads'}")
-        s0 = t.stride(0) if t.shape[0] > 1 else 0
-        s1 = t.stride(1) if t.shape[1] > 1 else 0
+        s0, s1, s2 = t.stride()
+        if shape[0] <= 1:
+            s0 = 0
+        if shape[1] <= 1:
+            s1 = 0
         p = t.data_ptr()
-        if t.numel() and (t.stride(2) != 1 or s0 % 8 or s1 % 8 or p % 16):
+        if (s2 != 1 or s0 % 8 or s1 % 8 or p % 16) and t.numel():
             raise ValueError(f"{name} needs contiguous channels, 16-byte aligned rows and strides "
                              f"that are multiples of 8")
         return _lib.KvRows(p, s0, s1)
@@ -108,11 +120,11 @@ class KVCache:
     def _attend_args(self, q, cu, seq_len, table, scale, with_lse, out):
         seqs = self._seqs(cu, seq_len, table)
         rows = self._rows("q", q)
-        S, Hq = q.shape[0], q.shape[1]
+        S, Hq, _ = q.shape
         if Hq < 1 or Hq % self.heads:
             raise ValueError(f"q's heads must be a multiple of the cache's {self.heads}")
         if out is None:
-            o = torch.empty((S, Hq, self.d), dtype=torch.bfloat16, device=self.device)
+            o = torch.empty((S, Hq, self.d), dtype=_BF16, device=self.device)
             lse = torch.empty((S, Hq), dtype=torch.float32, device=self.device) if with_lse else None
         else:
             o, lse = out
@@ -138,9 +150,6 @@ class KVCache:
                              f"on {self.device}")
         return workspace
 
-    def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
-
     # ---- calls
     def append(self, k, v, cu, seq_len, table, *, cos=None, sin=None, interleaved: bool = False,
                q=None, q_out=None):
@@ -161,7 +170,8 @@ class KVCache:
             if cos.dim() != 2 or cos.shape != sin.shape:
                 raise ValueError("cos and sin must be [positions, rot / 2]")
             for name, t in (("cos", cos), ("sin", sin)):
-                if t.dtype != torch.float32 or t.device != self.device or not t.is_contiguous():
+                if t.dtype is not torch.float32 or t.get_device() != self._gpu or \
+                        not t.is_contiguous():
                     raise ValueError(f"{name} must be contiguous float32 on {self.device}")
             rope_rows, rot = cos.shape[0], 2 * cos.shape[1]
             if rot % 16 or not 16 <= rot <= self.d or rope_rows < 1:
@@ -178,7 +188,7 @@ class KVCache:
             raise ValueError("q_out without q")
         rc = self._lib.indexer_kv_append(self._ref, seqs, rk, rv, N, _addr(cos), _addr(sin),
                                          rope_rows, rot, int(bool(interleaved)), rq, heads, ro,
-                                         self._stream())
+                                         _raw_stream(self._gpu))
         _lib.check(rc, "indexer_kv_append")
         return q_out
 
@@ -208,7 +218,7 @@ class KVCache:
         ws = self._workspace(n.value, workspace)
         rc = self._lib.indexer_kv_attend(self._ref, seqs, rows, S, Hq, scale, int(bool(causal)),
                                          max_len, o.data_ptr(), _addr(lse), _addr(ws),
-                                         0 if ws is None else ws.numel(), self._stream())
+                                         0 if ws is None else ws.numel(), _raw_stream(self._gpu))
         _lib.check(rc, "indexer_kv_attend")
         return (o, lse) if with_lse else o
 
@@ -233,7 +243,7 @@ class KVCache:
         if idx.dim() != 2 or idx.shape[0] != S or idx.shape[1] < 1 or tuple(valid_len.shape) != (S,):
             raise ValueError("idx must be [S, W] and valid_len [S]")
         for name, t in (("idx", idx), ("valid_len", valid_len), ("idx0", idx0)):
-            if t is not None and (t.dtype != torch.int32 or t.device != self.device or
+            if t is not None and (t.dtype is not _INT32 or t.get_device() != self._gpu or
                                   not t.is_contiguous()):
                 raise ValueError(f"{name} must be contiguous int32 on {self.device}")
         if idx0 is not None and tuple(idx0.shape) != (seqs.nseq,):
@@ -247,6 +257,6 @@ class KVCache:
         rc = self._lib.indexer_kv_attend_selected(
             self._ref, seqs, rows, S, Hq, scale, idx.data_ptr(), W, valid_len.data_ptr(),
             _addr(idx0), o.data_ptr(), _addr(lse), _addr(ws), 0 if ws is None else ws.numel(),
-            self._stream())
+            _raw_stream(self._gpu))
         _lib.check(rc, "indexer_kv_attend_selected")
         return (o, lse) if with_lse else o
