@@ -13,6 +13,7 @@ namespace {
 typedef __bf16 kvb8 __attribute__((ext_vector_type(8)));
 typedef __bf16 kvb2 __attribute__((ext_vector_type(2)));
 typedef float kvf4 __attribute__((ext_vector_type(4)));
+typedef uint32_t kvu4 __attribute__((ext_vector_type(4)));
 
 __device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 

@@ -65,7 +65,42 @@ __device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel)
     return __builtin_amdgcn_perm(hi, lo, sel);  // bytes 0-3 from lo, 4-7 from hi
 }
 
-// What a lane reads of a tile of 32 keys.
+// A tile of 32 keys and values on its way: read from memory with neighbouring
+// lanes on neighbouring 16-byte chunks of a row (the address unit takes four
+// lanes at a time and one cache line for each), then through LDS, private to
+// the wave, into the operands.
+template <int RB> struct Staged {
+    static constexpr int NCH = RB / 16;             // chunks of a row
+    static constexpr int RL = 64 / NCH;             // rows of a load
+    static constexpr int LD = 32 / RL;              // loads of a tile
+    kvu4 k[LD], v[LD];
+
+    // Chunk c of key row r lies at place c ^ swizzle(r), so that eight lanes
+    // reading one chunk of eight neighbouring rows meet in no bank.
+    __device__ static int swizzle(int r) { return NCH == 4 ? (r >> 2) & 3 : r & (NCH - 1); }
+
+    // off: byte offsets of the tile's rows; kb and vb point at the lane's chunk
+    __device__ void load(const char *kb, const char *vb, const uint64_t *off, int lane)
+    {
+#pragma unroll
+        for (int x = 0; x < LD; ++x) {
+            const uint64_t o = off[x * RL + lane / NCH];
+            k[x] = *reinterpret_cast<const kvu4 *>(kb + o);
+            v[x] = *reinterpret_cast<const kvu4 *>(vb + o);
+        }
+    }
+    __device__ void put(kvu4 *stage, int lane) const
+    {
+#pragma unroll
+        for (int x = 0; x < LD; ++x) {
+            const int r = x * RL + lane / NCH, c = lane % NCH;
+            stage[r * NCH + (c ^ swizzle(r))] = k[x];
+            stage[(32 + r) * NCH + c] = v[x];
+        }
+    }
+};
+
+// What a lane takes of a tile of 32 keys.
 template <bool FP8, int D> struct Tile {
     static constexpr int ES = FP8 ? 1 : 2;
     static constexpr int KU = D * ES / 64;          // 16-byte chunks of a key
@@ -73,27 +108,29 @@ template <bool FP8, int D> struct Tile {
     static constexpr int VW = D * ES / 64;          // dwords of D / 16 channels
     static constexpr int MT = D / 16;               // 16-channel tiles of O
     using VT = typename Words<VW>::T;
-    uint4 k[2][KU];
+    using ST = Staged<D * ES>;
+    kvu4 k[2][KU];
     VT v[8];
 
-    // off: byte offsets of the tile's rows in the cache
-    __device__ void load(const char *kb, const char *vb, const uint64_t *off, int m, int g)
+    __device__ void get_keys(const kvu4 *stage, int m, int g)
     {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(kb + off[16 * t + m]);
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int u = 0; u < KU; ++u) k[t][u] = p[4 * u];
-        }
+            for (int u = 0; u < KU; ++u)
+                k[t][u] = stage[(16 * t + m) * ST::NCH + ((4 * u + g) ^ ST::swizzle(16 * t + m))];
+    }
+    __device__ void get_values(const kvu4 *stage, int m, int g)
+    {
+        const VT *p = reinterpret_cast<const VT *>(stage + 32 * ST::NCH) + 4 * g * 16 + m;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = *reinterpret_cast<const VT *>(vb + off[16 * (j >> 2) + 4 * g + (j & 3)]);
+        for (int j = 0; j < 8; ++j) v[j] = p[((j & 3) + 16 * (j >> 2)) * 16];
     }
 
     __device__ kvb8 key(int t, int step) const
     {
         if constexpr (FP8) {
-            const uint4 &x = k[t][step >> 1];
+            const kvu4 x = k[t][step >> 1];
             const uint32_t a = step & 1 ? x.z : x.x, b = step & 1 ? x.w : x.y;
             const uint4 w = make_uint4(widen2<false>(a), widen2<true>(a), widen2<false>(b),
                                        widen2<true>(b));
@@ -144,6 +181,7 @@ template <bool FP8, int D, int NT, bool SEL>
 __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
 {
     using TL = Tile<FP8, D>;
+    using ST = typename TL::ST;
     constexpr int MT = TL::MT, CH = FP8 ? 4 : 2;  // channels that one dword of values holds
     constexpr int PITCH = D + 4;
     struct List {
@@ -152,7 +190,9 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
         uint32_t bad[kList / 32];       // which of a tile's keys are not there
     };
     struct Join { float o[4][16][PITCH]; };
-    __shared__ __align__(16) union { List list; Join join; } sm;
+    struct Work { List list; kvu4 stage[4][64 * ST::NCH]; };
+    __shared__ __align__(16) union { Work work; Join join; } smem;
+    Work &sm = smem.work;
     __shared__ float sm_m[4][16 * NT], sm_l[4][16 * NT];
 
     const KvCache &kc = p.c;
@@ -233,15 +273,17 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
         for (int i = 0; i < MT; ++i) o[t][i] = kvf4{0, 0, 0, 0};
     }
 
-    // a lane's part of a row: 16-byte chunks of a key from chunk g on, the D / 16
-    // channels of a value from D / 16 n on
-    const char *kb = static_cast<const char *>(kc.k) + g * 16;
-    const char *vb = static_cast<const char *>(kc.v) + n * (TL::VW * 4);
+    const char *kb = static_cast<const char *>(kc.k) + lane % ST::NCH * 16;
+    const char *vb = static_cast<const char *>(kc.v) + lane % ST::NCH * 16;
+    kvu4 *stage = sm.stage[wave];
     const int page_mask = (1 << kc.page_shift) - 1;
     const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
 
-    // One tile of 32 keys, s0 + at .. s0 + at + 31 of the entries.
-    auto process = [&](TL &cur, int s0, int at) KV_INLINE {
+    // The staged tile of 32 keys, s0 + at .. s0 + at + 31 of the entries.
+    auto process = [&](int s0, int at) KV_INLINE {
+        TL cur;
+        cur.get_keys(stage, n, g);
+        cur.get_values(stage, n, g);
         const uint32_t bad = (uint32_t)uniform((int)sm.list.bad[at >> 5]);
         const bool edge = !SEL && s0 + at + 32 > minlim;
         float ks[8], vs[8];
@@ -362,17 +404,13 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
         __syncthreads();
 
         // ---- tiles of 32 keys, in turn over the waves, the next one's loads ahead
-        TL a, b;
+        ST next;
         int at = wave * 32;
-        if (at < padded) a.load(kb, vb, sm.list.off + at, n, g);
-        while (at < padded) {
-            if (at + 128 < padded) b.load(kb, vb, sm.list.off + at + 128, n, g);
-            process(a, s0, at);
-            at += 128;
-            if (at >= padded) break;
-            if (at + 128 < padded) a.load(kb, vb, sm.list.off + at + 128, n, g);
-            process(b, s0, at);
-            at += 128;
+        if (at < padded) next.load(kb, vb, sm.list.off + at, lane);
+        for (; at < padded; at += 128) {
+            next.put(stage, lane);
+            if (at + 128 < padded) next.load(kb, vb, sm.list.off + at + 128, lane);
+            process(s0, at);
         }
     }
 
@@ -406,7 +444,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
                 x.y = o[t][w + 1][i] * f[t];
                 x.z = o[t][w + 2][i] * f[t];
                 x.w = o[t][w + 3][i] * f[t];
-                *reinterpret_cast<float4 *>(&sm.join.o[wave][n][MT * (4 * g + i) + w]) = x;
+                *reinterpret_cast<float4 *>(&smem.join.o[wave][n][MT * (4 * g + i) + w]) = x;
             }
         __syncthreads();
         // thread: column tid / 16, D / 16 channels
@@ -425,7 +463,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
                 if (sm_m[w][col] != -__builtin_inff())
                     sum += sm_l[w][col] * __builtin_amdgcn_exp2f(sm_m[w][col] - m4);
 #pragma unroll
-                for (int j = 0; j < C; ++j) y[j] += sm.join.o[w][cl][ch + j];
+                for (int j = 0; j < C; ++j) y[j] += smem.join.o[w][cl][ch + j];
             }
             const int64_t out = (row0 + tok) * p.q_heads + head * p.group + hh;
             // the row's own keys decide whether other blocks have a part of it
