@@ -51,11 +51,15 @@ struct KvAttendParams {
     int W;
     const int32_t *valid_len;
     const int32_t *idx0;      // [nseq] or null, subtracted from the entries
+    // selected positions of pairs of rows, as launch_kv_pick writes them (or
+    // null): per slot 2 W entries and their counts
+    uint32_t *pick;
+    int4 *pick_n;
     // the split: `chunk` keys a block, nsplit blocks along the keys; rows that
     // need more than one leave (o, m, l) in part_o / part_ml for the join
     int head_tile, groups;    // query heads of a key head that a block takes, blocks for all
     int tile_rows;            // query rows of a sequence that one block takes
-    int64_t slots;            // row tiles, empty ones among them
+    int64_t slot0, slots;     // row tiles of the launch, empty ones among them
     int chunk, nsplit;
     float *part_o;            // [nsplit, S, q_heads, d]
     float2 *part_ml;          // [nsplit, S, q_heads]
@@ -74,8 +78,11 @@ inline int64_t kv_blocks(const KvAttendParams &p)
 hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hipStream_t st);
 // 256 columns per block: many query rows
 hipError_t launch_kv_tiles(int dtype, int d, const KvAttendParams &p, hipStream_t st);
+// The lists of p.slots pairs of rows into p.pick (W at most kKvPairWidth)
+hipError_t launch_kv_pick(const KvAttendParams &p, hipStream_t st);
 hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st);
 
+constexpr int kKvPairWidth = 4096; // entries of a row that launch_kv_pick takes
 constexpr int kKvRowsCols = 32;   // columns of a launch_kv_rows block at most
 constexpr int kKvTileCols = 256;  // columns of a launch_kv_tiles block
 

@@ -102,7 +102,8 @@ dsai::KvCache kernel_cache(const indexer_kv_cache *c, const indexer_kv_seqs *s)
 // How a call is cut into blocks; depends on host sizes only, so that the
 // workspace functions and the calls agree.
 struct Plan {
-    bool tiles;
+    bool tiles, pairs;
+    int64_t pass;             // slots of a launch
     int nt, head_tile, groups, tile_rows, nsplit, chunk;
     int64_t slots, part_ml, bytes;
 };
@@ -120,6 +121,9 @@ constexpr int64_t kRaggedChunk = 4096;
 // sequence's rows go by blocks of 32 columns, straight from memory.
 constexpr int64_t kFewCols = 64;
 constexpr int kTilesHeads = 64;       // query heads of a key head in a block of 256 columns
+// Lists of one launch's pairs: 256 MB, about 16,000 pairs of 2,048 positions;
+// more rows take several launches.
+constexpr int64_t kPickBytes = int64_t(1) << 28;
 constexpr int64_t kFillTiles = 256;   // blocks of eight waves, one for each CU
 constexpr int64_t kMinTileChunk = 512;
 
@@ -141,6 +145,22 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
     }
     p.slots = selected ? S : S / p.tile_rows + nseq;
     const int64_t units = std::max<int64_t>(1, S / p.tile_rows) * c->heads * p.groups;
+    // Pairs of rows share what they both select: where 16 columns hold a row's
+    // heads and the pairs alone fill the GPU.
+    if (selected && group <= 16 && max_len <= dsai::kKvPairWidth && S >= 2 * (int64_t)nseq &&
+        S / 2 * c->heads >= kFillBlocks && c->pages * c->page <= (int64_t)UINT32_MAX) {
+        p.pairs = true;
+        p.tile_rows = 2;
+        p.nt = (int)div_up(2 * group, 16);
+        p.slots = S / 2 + nseq;
+        const int64_t each = 2 * max_len * 4 + 16;
+        p.pass = std::min(p.slots, std::max<int64_t>(kPickBytes / each, 1));
+        p.nsplit = 1;
+        p.chunk = INT32_MAX;
+        p.part_ml = round_up(p.pass * 2 * max_len * 4, 256);
+        p.bytes = p.part_ml + p.pass * 16;
+        return p;
+    }
     // parts that fill the GPU, as far as they are worth a block each; among
     // several sequences parts of at most kRaggedChunk keys, so that the longest
     // does not trail the others
@@ -154,6 +174,7 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
     if (nsplit <= 1) nsplit = 1, chunk = INT32_MAX;
     p.nsplit = (int)nsplit;
     p.chunk = (int)chunk;
+    p.pass = p.slots;
     if (nsplit > 1) {
         p.part_ml = round_up(nsplit * S * q_heads * c->d * 4, 256);
         p.bytes = p.part_ml + nsplit * S * q_heads * 8;
@@ -220,17 +241,26 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     p.head_tile = pl.head_tile;
     p.groups = pl.groups;
     p.tile_rows = pl.tile_rows;
-    p.slots = pl.slots;
     p.chunk = pl.chunk;
     p.nsplit = pl.nsplit;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + pl.part_ml);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = pl.tiles ? dsai::launch_kv_tiles(c->dtype, c->d, p, st)
-                            : dsai::launch_kv_rows(c->dtype, c->d, pl.nt, p, st);
-    if (e != hipSuccess) return fail_hip(e);
+    if (pl.pairs) {
+        p.pick = static_cast<uint32_t *>(workspace);
+        p.pick_n = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + pl.part_ml);
+    }
+    for (p.slot0 = 0; p.slot0 < pl.slots; p.slot0 += pl.pass) {
+        p.slots = std::min(pl.pass, pl.slots - p.slot0);
+        hipError_t e = hipSuccess;
+        if (pl.pairs) e = dsai::launch_kv_pick(p, st);
+        if (e != hipSuccess) return fail_hip(e);
+        e = pl.tiles ? dsai::launch_kv_tiles(c->dtype, c->d, p, st)
+                     : dsai::launch_kv_rows(c->dtype, c->d, pl.nt, p, st);
+        if (e != hipSuccess) return fail_hip(e);
+    }
     if (pl.nsplit > 1) {
-        e = dsai::launch_kv_join(c->d, p, st);
+        const hipError_t e = dsai::launch_kv_join(c->d, p, st);
         if (e != hipSuccess) return fail_hip(e);
     }
     return IDX_OK;

@@ -11,17 +11,17 @@
 // sequence times the head's query heads) and a range of the keys; its four
 // waves take turns at tiles of 32 keys, each with a softmax state of its own,
 // joined through LDS at the end.  Nothing but the list of key rows is shared in
-// the loop, so there is no barrier in it: keys and values go from memory to
-// registers and from there to the matrix unit.  Both products are computed
+// the loop, so there is no barrier in it: keys and values go from memory through
+// registers and a part of LDS of the wave's own to the matrix unit.  Both products are computed
 // transposed, S^T = K Q^T and O^T = V^T P^T:
 //  - the keys are the rows of A; lane (m, g) reads 16-byte chunks of key m, and
 //    the contraction takes the channels in the order in which they come;
 //  - S^T leaves lane (n, g) with the scores of column n against keys 4 g + i of
 //    both halves of the tile, which is the B operand of the second product when
 //    the contraction takes the keys in that order: P never leaves its lane;
-//  - V^T needs, for a channel, the values of those eight keys: lane (m, g) reads
-//    D / 16 neighbouring channels of each of them and transposes bytes
-//    (v_perm), then widens the codes exactly to bf16.
+//  - V^T needs, for a channel, the values of those eight keys: the transposing
+//    LDS reads (ds_read_b64_tr_b8, _b16) give them; codes are widened exactly to
+//    bf16.
 // P is rounded to bf16 for the matrix unit after it took the value page's scale
 // (relative 2^-9, as the rounding of the output); l sums the unrounded
 // probabilities.
@@ -39,37 +39,18 @@ constexpr float kSlack = 8.0f;          // log2 of the largest probability again
 constexpr int kFewParts = 16;           // parts that one wave joins
 constexpr float kLn2 = 0.693147180559945309f;
 
-template <int N> struct Words;          // N dwords that one load brings
-template <> struct Words<1> { using T = uint32_t; };
-template <> struct Words<2> { using T = uint2; };
-template <> struct Words<4> { using T = uint4; };
-
-__device__ inline uint32_t word(uint32_t x, int) { return x; }
-__device__ inline uint32_t word(const uint2 &x, int i) { return i ? x.y : x.x; }
-__device__ inline uint32_t word(const uint4 &x, int i)
-{
-    return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
-}
-__device__ inline void clear(uint32_t &x) { x = 0; }
-__device__ inline void clear(uint2 &x) { x = make_uint2(0, 0); }
-__device__ inline void clear(uint4 &x) { x = make_uint4(0, 0, 0, 0); }
-
 template <bool HI> __device__ inline uint32_t widen2(uint32_t w)
 {
     auto v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
     return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel)
-{
-    return __builtin_amdgcn_perm(hi, lo, sel);  // bytes 0-3 from lo, 4-7 from hi
-}
-
 // A tile of 32 keys and values on its way: read from memory with neighbouring
 // lanes on neighbouring 16-byte chunks of a row (the address unit takes four
 // lanes at a time and one cache line for each), then through LDS, private to
 // the wave, into the operands.
-template <int RB> struct Staged {
+template <bool FP8, int D> struct Staged {
+    static constexpr int RB = FP8 ? D : 2 * D;      // bytes of a row
     static constexpr int NCH = RB / 16;             // chunks of a row
     static constexpr int RL = 64 / NCH;             // rows of a load
     static constexpr int LD = 32 / RL;              // loads of a tile
@@ -78,6 +59,12 @@ template <int RB> struct Staged {
     // Chunk c of key row r lies at place c ^ swizzle(r), so that eight lanes
     // reading one chunk of eight neighbouring rows meet in no bank.
     __device__ static int swizzle(int r) { return NCH == 4 ? (r >> 2) & 3 : r & (NCH - 1); }
+    // Value rows likewise, for the 16 lanes of a transposing read: one chunk of
+    // keys 4 g .. 4 g + 3 and 16 + 4 g .. (8 bits), two of four keys (16 bits).
+    __device__ static int value_swizzle(int r)
+    {
+        return FP8 ? NCH == 8 ? (r & 3) | (r >> 2 & 4) : r >> 4 & 1 : NCH == 16 ? (r & 3) << 1 : r & 2;
+    }
 
     // off: byte offsets of the tile's rows; kb and vb point at the lane's chunk
     __device__ void load(const char *kb, const char *vb, const uint64_t *off, int lane)
@@ -89,13 +76,16 @@ template <int RB> struct Staged {
             v[x] = *reinterpret_cast<const kvu4 *>(vb + o);
         }
     }
-    __device__ void put(kvu4 *stage, int lane) const
+    // bad: rows that are not there; their values are 0, whatever was read
+    __device__ void put(kvu4 *stage, uint32_t bad, int lane) const
     {
 #pragma unroll
         for (int x = 0; x < LD; ++x) {
             const int r = x * RL + lane / NCH, c = lane % NCH;
             stage[r * NCH + (c ^ swizzle(r))] = k[x];
-            stage[(32 + r) * NCH + c] = v[x];
+            kvu4 y = v[x];
+            if (bad && (bad >> r & 1)) y = kvu4{0, 0, 0, 0};
+            stage[(32 + r) * NCH + (c ^ value_swizzle(r))] = y;
         }
     }
 };
@@ -105,12 +95,9 @@ template <bool FP8, int D> struct Tile {
     static constexpr int ES = FP8 ? 1 : 2;
     static constexpr int KU = D * ES / 64;          // 16-byte chunks of a key
     static constexpr int KS = D / 32;               // contraction steps of S
-    static constexpr int VW = D * ES / 64;          // dwords of D / 16 channels
     static constexpr int MT = D / 16;               // 16-channel tiles of O
-    using VT = typename Words<VW>::T;
-    using ST = Staged<D * ES>;
+    using ST = Staged<FP8, D>;
     kvu4 k[2][KU];
-    VT v[8];
 
     __device__ void get_keys(const kvu4 *stage, int m, int g)
     {
@@ -120,13 +107,6 @@ template <bool FP8, int D> struct Tile {
             for (int u = 0; u < KU; ++u)
                 k[t][u] = stage[(16 * t + m) * ST::NCH + ((4 * u + g) ^ ST::swizzle(16 * t + m))];
     }
-    __device__ void get_values(const kvu4 *stage, int m, int g)
-    {
-        const VT *p = reinterpret_cast<const VT *>(stage + 32 * ST::NCH) + 4 * g * 16 + m;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = p[((j & 3) + 16 * (j >> 2)) * 16];
-    }
-
     __device__ kvb8 key(int t, int step) const
     {
         if constexpr (FP8) {
@@ -140,49 +120,54 @@ template <bool FP8, int D> struct Tile {
         }
     }
 
-    // Channel `t` of the lane's D / 16 for its eight keys, t = NT q .. NT q +
-    // NT - 1 (NT channels of one dword).
-    __device__ void values(int q, kvb8 *a) const
+    // Channel 16 t + m of the lane's eight keys.  The reads transpose: of 16
+    // lanes each names 8 bytes, together 8 keys x 16 codes or 4 keys x 16 bf16
+    // values, and each gets one column.
+    __device__ static kvb8 value(const kvu4 *stage, int t, int m, int g)
     {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = word(v[j], q);
+        typedef __attribute__((address_space(3))) const char *Lds;
         if constexpr (FP8) {
-            uint32_t o[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 4 x 4 bytes: keys x channels -> channels x keys
-                const uint32_t *x = w + 4 * h;
-                const uint32_t a0 = perm(x[1], x[0], 0x05010400), a1 = perm(x[1], x[0], 0x07030602);
-                const uint32_t b0 = perm(x[3], x[2], 0x05010400), b1 = perm(x[3], x[2], 0x07030602);
-                o[h][0] = perm(b0, a0, 0x05040100);
-                o[h][1] = perm(b0, a0, 0x07060302);
-                o[h][2] = perm(b1, a1, 0x05040100);
-                o[h][3] = perm(b1, a1, 0x07060302);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint4 y = make_uint4(widen2<false>(o[0][t]), widen2<true>(o[0][t]),
-                                           widen2<false>(o[1][t]), widen2<true>(o[1][t]));
-                a[t] = __builtin_bit_cast(kvb8, y);
-            }
+            typedef int W2 __attribute__((ext_vector_type(2)));
+            typedef __attribute__((address_space(3))) W2 *P;
+            const int j = m >> 1, r = 16 * (j >> 2) + 4 * g + (j & 3);
+            const kvu4 *at = stage + (32 + r) * ST::NCH + (t ^ ST::value_swizzle(r));
+            const W2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((P)((Lds)at + 8 * (m & 1)));
+            const uint4 y = make_uint4(widen2<false>(w[0]), widen2<true>(w[0]), widen2<false>(w[1]),
+                                       widen2<true>(w[1]));
+            return __builtin_bit_cast(kvb8, y);
         } else {
+            typedef short W4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) W4 *P;
+            W4 w[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t sel = t ? 0x07060302 : 0x05040100;
-                const uint4 y = make_uint4(perm(w[1], w[0], sel), perm(w[3], w[2], sel),
-                                           perm(w[5], w[4], sel), perm(w[7], w[6], sel));
-                a[t] = __builtin_bit_cast(kvb8, y);
+            for (int h = 0; h < 2; ++h) {
+                const int r = 16 * h + 4 * g + (m >> 2), c = 2 * t + (m >> 1 & 1);
+                const kvu4 *at = stage + (32 + r) * ST::NCH + (c ^ ST::value_swizzle(r));
+                w[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)((Lds)at + 8 * (m & 1)));
             }
+            typedef short W8 __attribute__((ext_vector_type(8)));
+            const W8 y = __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(kvb8, y);
         }
     }
 };
 
-template <bool FP8, int D, int NT, bool SEL>
-__global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
+// What the rows of a block attend to: all of the sequence's tokens, one row's
+// selected positions, or the selections of two neighbouring rows as pick_kernel
+// laid them out (positions of both, of the first, of the second).
+enum { kAll = 0, kSelected = 1, kPairs = 2 };
+
+// Three blocks a CU where registers allow it and the keys come from the L2 (one
+// or two rows' selections: 752 us with three against 839 with two); streaming
+// all keys from memory two do better (99 against 105 us over 262,144 keys).
+template <bool FP8, int D, int NT, int MODE>
+__global__ __launch_bounds__(256, MODE != kAll && NT == 1 && FP8 ? 3 : 2)
+void rows_kernel(KvAttendParams p)
 {
+    constexpr bool SEL = MODE == kSelected, ALL = MODE == kAll, PAIR = MODE == kPairs;
     using TL = Tile<FP8, D>;
     using ST = typename TL::ST;
-    constexpr int MT = TL::MT, CH = FP8 ? 4 : 2;  // channels that one dword of values holds
+    constexpr int MT = TL::MT;
     constexpr int PITCH = D + 4;
     struct List {
         uint64_t off[kList];            // byte offsets of the keys' rows
@@ -204,7 +189,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
     const BlockAt blk = block_at(p);
     if (blk.none) return;
     const int head = blk.head, grp = blk.grp, split = blk.split;
-    const int64_t slot = blk.slot;
+    const int64_t slot = p.slot0 + blk.slot;
 
     const int R = SEL ? 1 : p.tile_rows;
     const int seq = SEL ? find_seq(kc.cu, kc.nseq, slot, 1, 0) : find_seq(kc.cu, kc.nseq, slot, R, 1);
@@ -217,9 +202,13 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
     const int64_t row0 = c0 + t0;
     // entries: keys 0 .. entries of the sequence, or of the row's selection
     int entries, base = 0;
+    int4 picked = {};            // positions of both rows, of the first, of the second
     if constexpr (SEL) {
         entries = clamped(p.valid_len[row0], p.W);
         base = p.idx0 ? p.idx0[seq] : 0;
+    } else if constexpr (PAIR) {
+        picked = p.pick_n[blk.slot];
+        entries = picked.x + picked.y + picked.z;
     } else {
         const int64_t last = p.causal ? (int64_t)len - rows_in_seq + t0 + ntok : len;
         entries = clamped(last < 0 ? 0 : (int)last, len);
@@ -230,18 +219,22 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
 
     // ---- the columns: query rows x heads
     kvb8 q[NT][TL::KS];
-    int lim[NT];                 // keys that the column sees
+    int lim[NT], end[NT];        // the column sees no entries from lim to end
     int minlim = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int col = 16 * t + n, tok = col / gsize, hh = grp * gsize + col % gsize;
         const bool in = tok < ntok && hh < p.group;
-        lim[t] = 0x7fffffff;
-        if constexpr (!SEL) {
+        lim[t] = end[t] = 0x7fffffff;
+        if constexpr (ALL) {
             if (in && p.causal) {
                 const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
                 lim[t] = x < 0 ? 0 : (int)x;
             }
+        }
+        if constexpr (PAIR) {
+            lim[t] = tok ? picked.x : picked.x + picked.y;
+            if (tok) end[t] = picked.x + picked.y;
         }
         minlim = lim[t] < minlim ? lim[t] : minlim;
         const uint16_t *src = p.q + (row0 + tok) * p.q_tok +
@@ -283,25 +276,17 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
     auto process = [&](int s0, int at) KV_INLINE {
         TL cur;
         cur.get_keys(stage, n, g);
-        cur.get_values(stage, n, g);
         const uint32_t bad = (uint32_t)uniform((int)sm.list.bad[at >> 5]);
         const bool edge = !SEL && s0 + at + 32 > minlim;
         float ks[8], vs[8];
-        if constexpr (FP8) {
+        auto factors = [&](const float *list, float (&f)[8]) KV_INLINE {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 a = *reinterpret_cast<const float4 *>(&sm.list.ks[at + 16 * h + 4 * g]);
-                const float4 b = *reinterpret_cast<const float4 *>(&sm.list.vs[at + 16 * h + 4 * g]);
-                ks[4 * h] = a.x; ks[4 * h + 1] = a.y; ks[4 * h + 2] = a.z; ks[4 * h + 3] = a.w;
-                vs[4 * h] = b.x; vs[4 * h + 1] = b.y; vs[4 * h + 2] = b.z; vs[4 * h + 3] = b.w;
+                const float4 a = *reinterpret_cast<const float4 *>(list + at + 16 * h + 4 * g);
+                f[4 * h] = a.x; f[4 * h + 1] = a.y; f[4 * h + 2] = a.z; f[4 * h + 3] = a.w;
             }
-        }
-        // keys that are not there: no score (below), and values that cannot be NaN
-        if (bad) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (bad >> (16 * (j >> 2) + 4 * g + (j & 3)) & 1) clear(cur.v[j]);
-        }
+        };
+        if constexpr (FP8) factors(sm.list.ks, ks);
         uint4 pk[NT];
         kvf4 acc[NT][2];
 #pragma unroll
@@ -314,6 +299,8 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
                     acc[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         a, q[t][s], s ? acc[t][h] : kvf4{0, 0, 0, 0}, 0, 0, 0);
             }
+        __builtin_amdgcn_sched_barrier(0);   // values after the scores: registers are short
+        if constexpr (FP8) factors(sm.list.vs, vs);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float x[8];
@@ -323,7 +310,9 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int key = 16 * (j >> 2) + 4 * g + (j & 3);
-                    if ((bad >> key & 1) || s0 + at + key >= lim[t]) x[j] = -__builtin_inff();
+                    const bool cut = PAIR ? s0 + at + key >= lim[t] && s0 + at + key < end[t]
+                                          : ALL && s0 + at + key >= lim[t];
+                    if ((bad >> key & 1) || cut) x[j] = -__builtin_inff();
                 }
             }
             float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
@@ -348,15 +337,12 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
                                pack_bf16(x[6], x[7]));
         }
 #pragma unroll
-        for (int w = 0; w < TL::VW; ++w) {
-            kvb8 a[CH];
-            cur.values(w, a);
+        for (int i = 0; i < MT; ++i) {
+            const kvb8 a = TL::value(stage, i, n, g);
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    o[t][CH * w + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        a[i], __builtin_bit_cast(kvb8, pk[t]), o[t][CH * w + i], 0, 0, 0);
+            for (int t = 0; t < NT; ++t)
+                o[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    a, __builtin_bit_cast(kvb8, pk[t]), o[t][i], 0, 0, 0);
         }
     };
 
@@ -377,10 +363,16 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
                 pos[k] = (int64_t)(there[k] ? p.idx[row0 * p.W + pos[k]] : -1) - base;
                 there[k] = there[k] && pos[k] >= 0 && pos[k] < len;
             }
+            if constexpr (PAIR)
+                pos[k] = there[k] ? p.pick[blk.slot * 2 * p.W + pos[k]] : 0;
         }
 #pragma unroll
-        for (int k = 0; k < kList / 256; ++k)
-            id[k] = there[k] ? (uint32_t)table[pos[k] >> kc.page_shift] : kNoPage;
+        for (int k = 0; k < kList / 256; ++k) {
+            if constexpr (PAIR)
+                id[k] = there[k] ? (uint32_t)(pos[k] >> kc.page_shift) : kNoPage;
+            else
+                id[k] = there[k] ? (uint32_t)table[pos[k] >> kc.page_shift] : kNoPage;
+        }
 #pragma unroll
         for (int k = 0; k < kList / 256; ++k) {
             const int i = tid + 256 * k;
@@ -408,7 +400,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
         int at = wave * 32;
         if (at < padded) next.load(kb, vb, sm.list.off + at, lane);
         for (; at < padded; at += 128) {
-            next.put(stage, lane);
+            next.put(stage, (uint32_t)uniform((int)sm.list.bad[at >> 5]), lane);
             if (at + 128 < padded) next.load(kb, vb, sm.list.off + at + 128, lane);
             process(s0, at);
         }
@@ -436,16 +428,10 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
     for (int t = 0; t < NT; ++t) {
         if (t > 0) __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int w = 0; w < MT; w += 4) {
-                float4 x;
-                x.x = o[t][w][i] * f[t];
-                x.y = o[t][w + 1][i] * f[t];
-                x.z = o[t][w + 2][i] * f[t];
-                x.w = o[t][w + 3][i] * f[t];
-                *reinterpret_cast<float4 *>(&smem.join.o[wave][n][MT * (4 * g + i) + w]) = x;
-            }
+        for (int w = 0; w < MT; ++w) {
+            const kvf4 x = o[t][w] * f[t];
+            *reinterpret_cast<kvf4 *>(&smem.join.o[wave][n][16 * w + 4 * g]) = x;
+        }
         __syncthreads();
         // thread: column tid / 16, D / 16 channels
         constexpr int C = D / 16;
@@ -468,7 +454,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(KvAttendParams p)
             const int64_t out = (row0 + tok) * p.q_heads + head * p.group + hh;
             // the row's own keys decide whether other blocks have a part of it
             int own = entries;
-            if constexpr (!SEL) {
+            if constexpr (ALL) {
                 if (p.causal) {
                     const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
                     own = x < 0 ? 0 : x < len ? (int)x : len;
@@ -569,15 +555,152 @@ __global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
         p.lse[unit] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_inff();
 }
 
+// The selections of the rows 2 i and 2 i + 1 of a sequence as three lists of
+// cache slots (page id * page size + slot): the positions of both rows, those
+// of the first only, those of the second only, each in ascending order.  Both
+// rows then share what rows_kernel reads of a common position, and all key
+// heads share the looking up of pages.  Two rows overlap where each finds the
+// other's position by bisection in LDS; a row that is not ascending, or that
+// names a position out of the sequence, shares nothing and keeps the rest of
+// its entries.  Bound by latency: about 15 us for 1,024 pairs of 2,048.
+__global__ __launch_bounds__(256) void pick_kernel(KvAttendParams p)
+{
+    constexpr int KM = kKvPairWidth / 256;
+    __shared__ int sm_row[2][kKvPairWidth];
+    __shared__ int sm_cnt[3][64];
+    __shared__ int sm_odd[4];
+    const KvCache &kc = p.c;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int64_t slot = p.slot0 + blockIdx.x;
+    const int seq = find_seq(kc.cu, kc.nseq, slot, 2, 1);
+    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
+    const int64_t t0 = (slot - (c0 / 2 + (int64_t)seq)) * 2;
+    if (t0 < 0 || t0 >= c1 - c0) return;
+    const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+    const int64_t row0 = c0 + t0;
+    const bool two = t0 + 1 < c1 - c0;
+    const int cnt[2] = {clamped(p.valid_len[row0], p.W), two ? clamped(p.valid_len[row0 + 1], p.W) : 0};
+    const int base = p.idx0 ? p.idx0[seq] : 0;
+    const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
+
+    // positions in LDS; the cache slot of each that exists in registers
+    uint32_t at[2][KM];
+    uint32_t here[2] = {0, 0};          // bit k: entry tid + 256 k exists
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        int pos[KM];
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            const int i = tid + 256 * k;
+            pos[k] = i < cnt[r] ? p.idx[(row0 + r) * p.W + i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            const int i = tid + 256 * k;
+            const int64_t x = (int64_t)pos[k] - base;
+            const bool in = i < cnt[r] && x >= 0 && x < len;
+            odd |= i < cnt[r] && !in;
+            pos[k] = in ? (int)x : -1;
+            at[r][k] = in ? (uint32_t)table[x >> kc.page_shift] : 0xffffffffu;
+            if (i < cnt[r]) sm_row[r][i] = in ? (int)x : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            if (at[r][k] < kc.pages && pos[k] >= 0) here[r] |= 1u << k;
+            at[r][k] = (at[r][k] << kc.page_shift) +
+                       ((uint32_t)pos[k] & ((1u << kc.page_shift) - 1));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            const int i = tid + 256 * k;
+            if (i + 1 < cnt[r]) odd |= sm_row[r][i] >= sm_row[r][i + 1];
+        }
+    const bool any = __ballot(odd) != 0;
+    if (lane == 0) sm_odd[wave] = any;
+    __syncthreads();
+    const bool apart = sm_odd[0] || sm_odd[1] || sm_odd[2] || sm_odd[3];
+
+    uint32_t both[2] = {0, 0};          // bit k: the other row has the position too
+    if (!apart && cnt[0] > 0 && cnt[1] > 0) {
+        // bisection in steps of a power of two, a thread's entries side by side
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int *other = sm_row[r ^ 1];
+            const int most = cnt[r ^ 1] - 1;
+            int x[KM], lo[KM];          // lo: the last entry known to be at most x, or 0
+#pragma unroll
+            for (int k = 0; k < KM; ++k) {
+                const int i = tid + 256 * k;
+                x[k] = i < cnt[r] ? sm_row[r][i] : -1;
+                lo[k] = 0;
+            }
+            int step = kKvPairWidth / 2;
+            while (step > most && step > 1) step >>= 1;
+            for (; step > 0; step >>= 1) {
+#pragma unroll
+                for (int k = 0; k < KM; ++k) {
+                    if (256 * k >= cnt[r]) continue;
+                    const int y = lo[k] + step;
+                    if (y <= most && other[y <= most ? y : most] <= x[k]) lo[k] = y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KM; ++k)
+                if (x[k] >= 0 && other[lo[k]] == x[k]) both[r] |= 1u << k;
+        }
+    }
+    if (!two) both[0] = ~0u;            // no second row: nothing to keep apart
+    const uint32_t list[3] = {here[0] & both[0], here[0] & ~both[0], here[1] & ~both[1]};
+#pragma unroll
+    for (int l = 0; l < 3; ++l)
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            const int c = __popcll(__ballot(list[l] >> k & 1));
+            if (lane == 0) sm_cnt[l][4 * k + wave] = c;
+        }
+    __syncthreads();
+    if (wave < 3) {                     // lists' entries before those of (k, wave)
+        const int c = lane < 4 * KM ? sm_cnt[wave][lane] : 0;
+        int sum = c;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const int y = __shfl_up(sum, s);
+            if (lane >= s) sum += y;
+        }
+        sm_cnt[wave][lane] = sum - c;
+        if (lane == 63) sm_odd[wave] = sum;
+    }
+    __syncthreads();
+    const int n[3] = {sm_odd[0], sm_odd[1], sm_odd[2]};
+    uint32_t *out = p.pick + blockIdx.x * 2 * (int64_t)p.W;
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int l = 0; l < 3; ++l) {
+        const int first = l == 0 ? 0 : l == 1 ? n[0] : n[0] + n[1];
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            const bool mine = list[l] >> k & 1;
+            const uint64_t b = __ballot(mine);
+            if (mine) out[first + sm_cnt[l][4 * k + wave] + __popcll(b & below)] = at[l == 2][k];
+        }
+    }
+    if (tid == 0) p.pick_n[blockIdx.x] = make_int4(n[0], n[1], n[2], 0);
+}
+
 template <bool FP8, int D>
 hipError_t launch_rows(int nt, const KvAttendParams &p, hipStream_t st)
 {
     const dim3 g((uint32_t)kv_blocks(p)), b(256);
-    const bool sel = p.idx != nullptr;
-#define ROWS(NT)                                                     \
-    case NT:                                                         \
-        if (sel) rows_kernel<FP8, D, NT, true><<<g, b, 0, st>>>(p);  \
-        else rows_kernel<FP8, D, NT, false><<<g, b, 0, st>>>(p);     \
+#define ROWS(NT)                                                                  \
+    case NT:                                                                      \
+        if (p.pick) rows_kernel<FP8, D, NT, kPairs><<<g, b, 0, st>>>(p);          \
+        else if (p.idx) rows_kernel<FP8, D, NT, kSelected><<<g, b, 0, st>>>(p);   \
+        else rows_kernel<FP8, D, NT, kAll><<<g, b, 0, st>>>(p);                   \
         break
     switch (nt) {
         ROWS(1);
@@ -596,6 +719,12 @@ hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hip
     if (d == 64) return fp8 ? launch_rows<true, 64>(nt, p, st) : launch_rows<false, 64>(nt, p, st);
     if (d == 128) return fp8 ? launch_rows<true, 128>(nt, p, st) : launch_rows<false, 128>(nt, p, st);
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_pick(const KvAttendParams &p, hipStream_t st)
+{
+    pick_kernel<<<dim3((uint32_t)p.slots), 256, 0, st>>>(p);
+    return hipGetLastError();
 }
 
 hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st)

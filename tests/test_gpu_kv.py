@@ -242,6 +242,16 @@ SELECTED = [
 ]
 
 
+PAIRS = [
+    # many rows and few heads a key head: two neighbouring rows share their positions
+    (FP8, 128, 64, 8, 8, [300], [151], 65),
+    (BF16, 64, 16, 4, 5, [333, 41, 0, 200], [160, 41, 3, 101], 40),
+    (FP8, 64, 32, 16, 16, [500, 90], [64, 3], 129),
+    (BF16, 128, 128, 2, 3, [700], [513], 70),
+    (FP8, 128, 16, 1, 1, [260, 300], [512, 515], 33),
+]
+
+
 def selection(g, S, W, cu, lens, idx0=None):
     idx = np.full((S, W), -1, np.int32)
     vl = np.zeros(S, np.int32)
@@ -278,6 +288,46 @@ def test_selected_matches_the_reference(c, offset):
     pr.gpu().attend_selected(q.to(DEV), dev(idx), dev(vl), dev(cu), dev(pr.lens), dev(pr.table),
                              idx0=None if idx0 is None else dev(idx0), with_lse=True,
                              out=(out, lse))
+    torch.cuda.synchronize()
+    check(out, lse, ref, d, str(c))
+    assert bool((out[S - pad:] == 7).all()) and bool((lse[S - pad:] == 7).all())
+
+
+@pytest.mark.parametrize("c", PAIRS, ids=range(len(PAIRS)))
+def test_neighbouring_rows_that_share_positions(c):
+    """Rows that drift from one to the next, some without entries, some with
+    entries of no token, out of order or twice, next to ordinary ones."""
+    dtype, d, page, heads, group, lens, rows, W = c
+    log(c)
+    pr = Problem(d + W + 1, dtype, heads, d, page, lens, pow2=True)
+    pad = 3
+    S = sum(rows) + pad
+    cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    idx0 = (np.arange(len(lens)) * 1000 + 5).astype(np.int32)
+    idx, vl = np.full((S, W), -1, np.int32), np.zeros(S, np.int32)
+    for i, L in enumerate(lens):
+        score = pr.g.standard_normal(L)
+        for r in range(cu[i], cu[i + 1]):
+            score += 0.3 * pr.g.standard_normal(L)
+            n = min(W, L) if r % 5 else int(pr.g.integers(0, min(W, L) + 1))
+            if r % 11 == 3:
+                n = 0
+            sel = np.sort(np.argsort(-score)[:n]) + idx0[i]
+            if r % 7 == 2 and n > 12:
+                sel[3], sel[5], sel[9] = -1, 10 ** 9, sel[8]
+            if r % 7 == 4:
+                sel = sel[::-1]
+            idx[r, :n], vl[r] = sel, n
+    pr.table[0, 1] = 10 ** 6                                     # a page that is not there
+    q = pr.queries(S, heads * group)
+    ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
+                     pr.cache["v"], pr.scale["v"], d ** -0.5, idx=idx, valid_len=vl, idx0=idx0)
+    out = torch.full((S, heads * group, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((S, heads * group), 7.0, device=DEV)
+    cache = pr.gpu()
+    args = (q.to(DEV), dev(idx), dev(vl), dev(cu), dev(pr.lens), dev(pr.table))
+    assert cache.attend_selected_workspace_bytes(S, heads * group, len(lens), W) > 0
+    cache.attend_selected(*args, idx0=dev(idx0), with_lse=True, out=(out, lse))
     torch.cuda.synchronize()
     check(out, lse, ref, d, str(c))
     assert bool((out[S - pad:] == 7).all()) and bool((lse[S - pad:] == 7).all())
