@@ -36,6 +36,8 @@ namespace {
 constexpr int kList = 1024;             // keys resolved to rows at a time
 constexpr uint32_t kNoPage = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 of the largest probability against the running maximum
+constexpr int kPickThreads = 512;       // kKvPairWidth / 512 entries of a row each
+constexpr int kPickBits = 1 << 17;      // positions that a row's bitmap covers at a time
 constexpr int kFewParts = 16;           // parts that one wave joins
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -557,18 +559,18 @@ __global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
 
 // The selections of the rows 2 i and 2 i + 1 of a sequence as three lists of
 // cache slots (page id * page size + slot): the positions of both rows, those
-// of the first only, those of the second only, each in ascending order.  Both
+// of the first only, those of the second only, each in the row's order.  Both
 // rows then share what rows_kernel reads of a common position, and all key
-// heads share the looking up of pages.  Two rows overlap where each finds the
-// other's position by bisection in LDS; a row that is not ascending, or that
-// names a position out of the sequence, shares nothing and keeps the rest of
-// its entries.  Bound by latency: about 15 us for 1,024 pairs of 2,048.
-__global__ __launch_bounds__(256) void pick_kernel(KvAttendParams p)
+// heads share the looking up of pages.  Whether the other row has a position is
+// read from its bitmap in LDS, kPickBits positions at a time; rows that name a
+// position twice share nothing.  Positions out of the sequence and on pages
+// that do not exist are dropped.
+__global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
 {
-    constexpr int KM = kKvPairWidth / 256;
-    __shared__ int sm_row[2][kKvPairWidth];
+    constexpr int KM = kKvPairWidth / kPickThreads;
+    __shared__ __align__(16) uint32_t sm_bits[2][kPickBits / 32];
     __shared__ int sm_cnt[3][64];
-    __shared__ int sm_odd[4];
+    __shared__ int sm_odd[8];
     const KvCache &kc = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t slot = p.slot0 + blockIdx.x;
@@ -583,77 +585,79 @@ __global__ __launch_bounds__(256) void pick_kernel(KvAttendParams p)
     const int base = p.idx0 ? p.idx0[seq] : 0;
     const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
 
-    // positions in LDS; the cache slot of each that exists in registers
-    uint32_t at[2][KM];
-    uint32_t here[2] = {0, 0};          // bit k: entry tid + 256 k exists
-    bool odd = false;
+    int pos[2][KM];                     // -1: no such position
+    uint32_t at[2][KM];                 // its cache slot
+    uint32_t here[2] = {0, 0};          // bit k: entry tid + 256 k has one
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        int pos[KM];
+        const int32_t *src = p.idx + (row0 + (two ? r : 0)) * p.W;
+        const int last = cnt[r] > 0 ? cnt[r] - 1 : 0;   // loads without branches between them
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
-            const int i = tid + 256 * k;
-            pos[k] = i < cnt[r] ? p.idx[(row0 + r) * p.W + i] : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < KM; ++k) {
-            const int i = tid + 256 * k;
-            const int64_t x = (int64_t)pos[k] - base;
-            const bool in = i < cnt[r] && x >= 0 && x < len;
-            odd |= i < cnt[r] && !in;
-            pos[k] = in ? (int)x : -1;
-            at[r][k] = in ? (uint32_t)table[x >> kc.page_shift] : 0xffffffffu;
-            if (i < cnt[r]) sm_row[r][i] = in ? (int)x : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < KM; ++k) {
-            if (at[r][k] < kc.pages && pos[k] >= 0) here[r] |= 1u << k;
-            at[r][k] = (at[r][k] << kc.page_shift) +
-                       ((uint32_t)pos[k] & ((1u << kc.page_shift) - 1));
+            if (kPickThreads * k >= cnt[r]) continue;
+            const int i = tid + kPickThreads * k;
+            pos[r][k] = src[i < last ? i : last];
         }
     }
-    __syncthreads();
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
-            const int i = tid + 256 * k;
-            if (i + 1 < cnt[r]) odd |= sm_row[r][i] >= sm_row[r][i + 1];
+            at[r][k] = 0xffffffffu;
+            if (kPickThreads * k >= cnt[r]) {
+                pos[r][k] = -1;
+                continue;
+            }
+            const int64_t x = (int64_t)pos[r][k] - base;
+            const bool in = tid + kPickThreads * k < cnt[r] && x >= 0 && x < len;
+            pos[r][k] = in ? (int)x : -1;
+            at[r][k] = (uint32_t)table[in ? x >> kc.page_shift : 0];
         }
-    const bool any = __ballot(odd) != 0;
-    if (lane == 0) sm_odd[wave] = any;
-    __syncthreads();
-    const bool apart = sm_odd[0] || sm_odd[1] || sm_odd[2] || sm_odd[3];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            if (at[r][k] >= kc.pages) pos[r][k] = -1;
+            if (pos[r][k] >= 0) here[r] |= 1u << k;
+            at[r][k] = (at[r][k] << kc.page_shift) +
+                       ((uint32_t)pos[r][k] & ((1u << kc.page_shift) - 1));
+        }
 
     uint32_t both[2] = {0, 0};          // bit k: the other row has the position too
-    if (!apart && cnt[0] > 0 && cnt[1] > 0) {
-        // bisection in steps of a power of two, a thread's entries side by side
+    bool twice = false;
+    if (cnt[0] > 0 && cnt[1] > 0) {
+        for (int w0 = 0; w0 < len; w0 += kPickBits) {
+            if (w0 > 0) __syncthreads();
+            for (int i = tid; i < 2 * kPickBits / 128; i += kPickThreads)
+                reinterpret_cast<uint4 *>(sm_bits)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int *other = sm_row[r ^ 1];
-            const int most = cnt[r ^ 1] - 1;
-            int x[KM], lo[KM];          // lo: the last entry known to be at most x, or 0
-#pragma unroll
-            for (int k = 0; k < KM; ++k) {
-                const int i = tid + 256 * k;
-                x[k] = i < cnt[r] ? sm_row[r][i] : -1;
-                lo[k] = 0;
-            }
-            int step = kKvPairWidth / 2;
-            while (step > most && step > 1) step >>= 1;
-            for (; step > 0; step >>= 1) {
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int k = 0; k < KM; ++k) {
-                    if (256 * k >= cnt[r]) continue;
-                    const int y = lo[k] + step;
-                    if (y <= most && other[y <= most ? y : most] <= x[k]) lo[k] = y;
+                    const uint32_t x = (uint32_t)(pos[r][k] - w0);
+                    if (kPickThreads * k < cnt[r] && pos[r][k] >= 0 && x < (uint32_t)kPickBits)
+                        twice |= atomicOr(&sm_bits[r][x >> 5], 1u << (x & 31)) >> (x & 31) & 1;
                 }
-            }
+            __syncthreads();
 #pragma unroll
-            for (int k = 0; k < KM; ++k)
-                if (x[k] >= 0 && other[lo[k]] == x[k]) both[r] |= 1u << k;
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int k = 0; k < KM; ++k) {
+                    const uint32_t x = (uint32_t)(pos[r][k] - w0);
+                    if (kPickThreads * k < cnt[r] && pos[r][k] >= 0 && x < (uint32_t)kPickBits)
+                        both[r] |= (sm_bits[r ^ 1][x >> 5] >> (x & 31) & 1) << k;
+                }
         }
     }
+    const bool any = __ballot(twice) != 0;
+    if (lane == 0) sm_odd[wave] = any;
+    __syncthreads();
+    bool apart = false;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) apart |= sm_odd[w] != 0;
+    if (apart) both[0] = both[1] = 0;
+    __syncthreads();
     if (!two) both[0] = ~0u;            // no second row: nothing to keep apart
     const uint32_t list[3] = {here[0] & both[0], here[0] & ~both[0], here[1] & ~both[1]};
 #pragma unroll
@@ -661,11 +665,11 @@ __global__ __launch_bounds__(256) void pick_kernel(KvAttendParams p)
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
             const int c = __popcll(__ballot(list[l] >> k & 1));
-            if (lane == 0) sm_cnt[l][4 * k + wave] = c;
+            if (lane == 0) sm_cnt[l][8 * k + wave] = c;
         }
     __syncthreads();
     if (wave < 3) {                     // lists' entries before those of (k, wave)
-        const int c = lane < 4 * KM ? sm_cnt[wave][lane] : 0;
+        const int c = lane < 8 * KM ? sm_cnt[wave][lane] : 0;
         int sum = c;
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) {
@@ -686,7 +690,7 @@ __global__ __launch_bounds__(256) void pick_kernel(KvAttendParams p)
         for (int k = 0; k < KM; ++k) {
             const bool mine = list[l] >> k & 1;
             const uint64_t b = __ballot(mine);
-            if (mine) out[first + sm_cnt[l][4 * k + wave] + __popcll(b & below)] = at[l == 2][k];
+            if (mine) out[first + sm_cnt[l][8 * k + wave] + __popcll(b & below)] = at[l == 2][k];
         }
     }
     if (tid == 0) p.pick_n[blockIdx.x] = make_int4(n[0], n[1], n[2], 0);
@@ -723,7 +727,7 @@ hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hip
 
 hipError_t launch_kv_pick(const KvAttendParams &p, hipStream_t st)
 {
-    pick_kernel<<<dim3((uint32_t)p.slots), 256, 0, st>>>(p);
+    pick_kernel<<<dim3((uint32_t)p.slots), kPickThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
