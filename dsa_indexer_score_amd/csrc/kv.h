@@ -32,7 +32,7 @@ struct KvAppendParams {
     int rot, interleaved;
     int q_heads;              // 0: no queries
     int64_t N;                // new tokens
-    int64_t kv_units, q_units;
+    int64_t kv_blocks;        // blocks of pages, before those of queries
 };
 
 struct KvAttendParams {

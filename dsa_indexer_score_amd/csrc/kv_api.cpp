@@ -316,9 +316,8 @@ int indexer_kv_append(const indexer_kv_cache *c, const indexer_kv_seqs *s,
     p.N = N;
     // A sequence of n new tokens touches at most n / page + 2 pages; with
     // page slots numbered from cu / page + 2 i, sequence i has that many.
-    p.kv_units = (N / c->page + 2 * (int64_t)s->nseq) * c->heads * 2;
-    p.q_units = q_heads > 0 ? N : 0;
-    if (p.kv_units + p.q_units >= INT32_MAX) return IDX_EUNSUPPORTED;
+    p.kv_blocks = (N / c->page + 2 * (int64_t)s->nseq) * div_up(c->heads, 4) * 2;
+    if (p.kv_blocks + N >= INT32_MAX) return IDX_EUNSUPPORTED;
     DeviceGuard guard(c->device);
     if (guard.err != hipSuccess) return fail_hip(guard.err);
     const hipError_t e = dsai::launch_kv_append(c->dtype, c->d, p, static_cast<hipStream_t>(stream));

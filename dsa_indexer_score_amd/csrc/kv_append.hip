@@ -9,10 +9,12 @@
 // the change of scale exact but for codes that fall below the smallest normal
 // one, which are rounded to nearest even once more.
 //
-// One wave takes one (page, key head) of the keys or of the values, so nothing
-// is shared between waves: it keeps the page's new tokens in registers (16 KB
-// at 64 tokens of 128), reduces their maximum and writes them once.  Bound by
-// memory: every input is read once and every code written once.  The rotation
+// One wave takes one (page, key head) of the keys or of the values: it keeps the
+// page's new tokens in registers (16 KB at 64 tokens of 128), reduces their
+// maximum and writes them once.  Four heads of a page make a block, which keeps
+// the page's cosines and sines in LDS.  The queries of a token are one wave's.
+// Bound by memory: every input is read once and every output written once,
+// loads first, so that a wave has 8 to 16 KB in flight.  The rotation
 // is computed without contraction into fused multiply-adds (each product is
 // rounded to fp32 and the sum again), so that a key's code does not depend on
 // how the compiler pairs operations.
@@ -34,9 +36,8 @@ __device__ inline float pow2_scale(float amax)
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ inline void unpack8(const uint4 &x, float (&f)[8])
+__device__ inline void unpack8(const kvu4 w, float (&f)[8])
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f[2 * i] = __uint_as_float(w[i] << 16);
@@ -44,10 +45,10 @@ __device__ inline void unpack8(const uint4 &x, float (&f)[8])
     }
 }
 
-__device__ inline uint4 pack8(const float (&f)[8])
+__device__ inline kvu4 pack8(const float (&f)[8])
 {
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                      pack_bf16(f[6], f[7]));
+    return kvu4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                pack_bf16(f[6], f[7])};
 }
 
 __device__ inline uint2 codes8(const float (&f)[8])
@@ -60,80 +61,63 @@ __device__ inline uint2 codes8(const float (&f)[8])
     return make_uint2(a, b);
 }
 
-// The rotation of the 8 channels [8 c, 8 c + 8) that a lane holds of one row.
-// Lanes of one row are neighbours; with halves, channel i pairs with i +
-// rot / 2, which another lane of the row holds (rot is a multiple of 16).
-// Every lane of the wave has to call it.
-struct Turn {
-    float cs[8], sn[8];
-    bool on;
-
-    __device__ void load(const KvAppendParams &p, int64_t pos, int c)
-    {
-        const int half = p.rot >> 1;
-        on = p.cos && 8 * c < p.rot;
-        if (!on) return;
-        if (p.interleaved) {
-            const float4 a = *reinterpret_cast<const float4 *>(p.cos + pos * half + 4 * c);
-            const float4 b = *reinterpret_cast<const float4 *>(p.sin + pos * half + 4 * c);
-            cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
-            sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
-        } else {
-            const int at = 8 * c < half ? 8 * c : 8 * c - half;
-            const float4 *a = reinterpret_cast<const float4 *>(p.cos + pos * half + at);
-            const float4 *b = reinterpret_cast<const float4 *>(p.sin + pos * half + at);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 x = a[i], y = b[i];
-                cs[4 * i] = x.x; cs[4 * i + 1] = x.y; cs[4 * i + 2] = x.z; cs[4 * i + 3] = x.w;
-                sn[4 * i] = y.x; sn[4 * i + 1] = y.y; sn[4 * i + 2] = y.z; sn[4 * i + 3] = y.w;
-            }
-        }
-    }
-
-    __device__ void apply(const KvAppendParams &p, const uint4 &x, int c, float (&f)[8]) const
-    {
-#pragma clang fp contract(off)
-        unpack8(x, f);
-        if (!p.cos) return;
-        if (p.interleaved) {
-            if (!on) return;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = f[2 * i], b = f[2 * i + 1];
-                const float ac = a * cs[i], bs = b * sn[i], bc = b * cs[i], as = a * sn[i];
-                f[2 * i] = ac - bs;
-                f[2 * i + 1] = bc + as;
-            }
-            return;
-        }
-        const int hop = p.rot >> 4;          // lanes between the halves
-        const bool first = 8 * c < (p.rot >> 1);
-        const int lane = threadIdx.x & 63;
-        const int from = !on ? lane : first ? lane + hop : lane - hop;
-        uint4 y;
-        y.x = __shfl(x.x, from);
-        y.y = __shfl(x.y, from);
-        y.z = __shfl(x.z, from);
-        y.w = __shfl(x.w, from);
-        float o[8];
-        unpack8(y, o);
-        if (!on) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float own = f[i] * cs[i], other = o[i] * sn[i];
-            f[i] = first ? own - other : own + other;
-        }
-    }
-};
-
-// One (page, head) of the keys (which = 0) or the values (which = 1).
-template <bool FP8, int D, int PAGE>
-__device__ inline void append_page(const KvAppendParams &p, int64_t slot, int head, int which)
+// The rotation of the 8 channels [8 c, 8 c + 8) that a lane holds of one row,
+// by 8 cosines and sines (interleaved pairs: the first 4).  Lanes of one row are
+// neighbours; with halves, channel i pairs with i + rot / 2, which another lane
+// of the row holds (rot is a multiple of 16).  Every lane of the wave has to
+// call it.
+__device__ inline void turn(const KvAppendParams &p, const kvu4 x, int c, const kvf4 (&cs)[2],
+                            const kvf4 (&sn)[2], float (&f)[8])
 {
-    constexpr int L = D / 8, ROWS = 64 / L, NIT = PAGE / ROWS;  // lanes a row, rows a step
+#pragma clang fp contract(off)
+    unpack8(x, f);
+    const bool on = 8 * c < p.rot;
+    if (p.interleaved) {
+        if (!on) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = f[2 * i], b = f[2 * i + 1];
+            const float ac = a * cs[0][i], bs = b * sn[0][i], bc = b * cs[0][i], as = a * sn[0][i];
+            f[2 * i] = ac - bs;
+            f[2 * i + 1] = bc + as;
+        }
+        return;
+    }
+    const int hop = p.rot >> 4;              // lanes between the halves
+    const bool first = 8 * c < (p.rot >> 1);
+    const int lane = threadIdx.x & 63;
+    const int from = !on ? lane : first ? lane + hop : lane - hop;
+    kvu4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __shfl(x[i], from);
+    float o[8];
+    unpack8(y, o);
+    if (!on) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float own = f[i] * cs[i >> 2][i & 3], other = o[i] * sn[i >> 2][i & 3];
+        f[i] = first ? own - other : own + other;
+    }
+}
+
+// Where the lane's cosines and sines start in a row of rot / 2.
+__device__ inline int turn_at(const KvAppendParams &p, int c)
+{
+    if (8 * c >= p.rot) return 0;
+    if (p.interleaved) return 4 * c;
+    return 8 * c < (p.rot >> 1) ? 8 * c : 8 * c - (p.rot >> 1);
+}
+
+// One page of up to four heads of the keys (which = 0) or the values (1).
+template <bool FP8, int D, int PAGE>
+__device__ inline void append_page(const KvAppendParams &p, int64_t slot, int head0, int which,
+                                   float *rope)
+{
+    constexpr int L = D / 8, ROWS = 64 / L;                    // lanes a row, rows a step
+    constexpr int NIT = PAGE / ROWS;
     const KvCache &kc = p.c;
-    const int lane = threadIdx.x & 63, c = lane % L, r = lane / L;
+    const int tid = threadIdx.x, lane = tid & 63, c = lane % L, r = lane / L;
+    const int head = head0 + uniform(tid >> 6);
     const int i = find_seq(kc.cu, kc.nseq, slot, PAGE, 2);
     const int c0 = clamped(kc.cu[i], p.N), n = clamped(kc.cu[i + 1], p.N) - c0;
     const int cap = kc.table_width * PAGE;                      // < 2^31, checked on the host
@@ -143,49 +127,71 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
     int64_t end = (int64_t)held + (n > 0 ? n : 0);
     end = end < cap ? end : cap;
     if (p.cos && end > p.rope_rows) end = p.rope_rows;
-    if (pg < held / PAGE || pg * PAGE >= end || held >= end) return;
+    if (pg < held / PAGE || pg * PAGE >= end || held >= end) return;   // the whole block
     const uint32_t id = (uint32_t)kc.table[(int64_t)i * kc.table_stride + pg];
     if (id >= kc.pages) return;
     const int s0 = pg * PAGE > held ? 0 : held - (int)pg * PAGE;       // slots to fill
     const int s1 = (int)(end - pg * PAGE < PAGE ? end - pg * PAGE : PAGE);
-    const int64_t unit = (int64_t)id * kc.heads + head;
-    const uint16_t *src = p.src[which] + head * p.head_stride[which] + 8 * c;
-    const int64_t tok0 = c0 + (pg * PAGE - held);                      // token of slot 0
+    const bool mine = head < kc.heads;
+    const int64_t unit = (int64_t)id * kc.heads + (mine ? head : 0);
+    const int64_t ts = p.tok_stride[which];
+    const uint16_t *src = p.src[which] + (mine ? head : 0) * p.head_stride[which] + 8 * c +
+                          (c0 + (pg * PAGE - held)) * ts;              // slot 0's token
+    const bool turns = which == 0 && p.cos;
+
+    // all rows' loads first; lanes behind the last row read it again
+    kvu4 x[NIT];
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+        const int s = s0 + it * ROWS, at = s + r < s1 ? s + r : s1 - 1;
+        if (s < s1) x[it] = *reinterpret_cast<const kvu4 *>(src + at * ts);
+    }
+    const int half = p.rot >> 1;
+    if (turns) {                         // the page's cosines and sines, for all its heads
+        const int total = (s1 - s0) * half;
+        const float *cs = p.cos + (pg * PAGE + s0) * half, *sn = p.sin + (pg * PAGE + s0) * half;
+        for (int k = 4 * tid; k < total; k += 1024) {
+            *reinterpret_cast<kvf4 *>(rope + k) = *reinterpret_cast<const kvf4 *>(cs + k);
+            *reinterpret_cast<kvf4 *>(rope + total + k) = *reinterpret_cast<const kvf4 *>(sn + k);
+        }
+        __syncthreads();
+        rope += turn_at(p, c);
+    }
+    if (!mine) return;
+    auto rotated = [&](int it, float (&f)[8]) KV_INLINE {
+        if (!turns) {
+            unpack8(x[it], f);
+            return;
+        }
+        const int at = it * ROWS + r < s1 - s0 ? it * ROWS + r : s1 - s0 - 1;
+        const kvf4 *cp = reinterpret_cast<const kvf4 *>(rope + at * half);
+        const kvf4 *sp = reinterpret_cast<const kvf4 *>(rope + (s1 - s0 + at) * half);
+        const kvf4 cs[2] = {cp[0], p.interleaved ? cp[0] : cp[1]};
+        const kvf4 sn[2] = {sp[0], p.interleaved ? sp[0] : sp[1]};
+        turn(p, x[it], c, cs, sn, f);
+    };
 
     if constexpr (!FP8) {
-        uint4 *dst = reinterpret_cast<uint4 *>(which ? kc.v : kc.k) + unit * PAGE * L + c;
-        for (int s = s0; s < s1; s += ROWS) {
-            const int at = s + r;
-            const bool in = at < s1;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (in) x = *reinterpret_cast<const uint4 *>(src + (tok0 + at) * p.tok_stride[which]);
-            if (which == 0) {
-                Turn t;
-                t.load(p, pg * PAGE + (in ? at : s), c);
+        kvu4 *dst = reinterpret_cast<kvu4 *>(which ? kc.v : kc.k) + unit * PAGE * L + c;
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+            const int s = s0 + it * ROWS, at = s + r;
+            if (s >= s1) continue;                                     // the whole wave
+            kvu4 y = x[it];
+            if (turns) {
                 float f[8];
-                t.apply(p, x, c, f);
-                x = pack8(f);
+                rotated(it, f);
+                y = pack8(f);
             }
-            if (in) dst[(int64_t)at * L] = x;
+            if (at < s1) dst[at * L] = y;
         }
-        return;
     } else {
         float f[NIT][8];
         float amax = 0.0f;
 #pragma unroll
         for (int it = 0; it < NIT; ++it) {
-            const int s = s0 + it * ROWS, at = s + r;
-            if (s >= s1) continue;                                     // the whole wave
-            const bool in = at < s1;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (in) x = *reinterpret_cast<const uint4 *>(src + (tok0 + at) * p.tok_stride[which]);
-            if (which == 0) {
-                Turn t;
-                t.load(p, pg * PAGE + (in ? at : s), c);
-                t.apply(p, x, c, f[it]);
-            } else {
-                unpack8(x, f[it]);
-            }
+            if (s0 + it * ROWS >= s1) continue;                        // the whole wave
+            rotated(it, f[it]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 // infinities and NaN become the code NaN and do not move the scale
@@ -207,7 +213,7 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
             } else {                                                   // the held tokens' codes
                 const float ratio = old / s;
                 for (int at = r; at < s0; at += ROWS) {
-                    const uint2 w = dst[(int64_t)at * L];
+                    const uint2 w = dst[at * L];
                     float g[8];
                     const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
@@ -219,7 +225,7 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
                         g[4 * j + 2] = hi[0] * ratio;
                         g[4 * j + 3] = hi[1] * ratio;
                     }
-                    dst[(int64_t)at * L] = codes8(g);
+                    dst[at * L] = codes8(g);
                 }
             }
         }
@@ -231,17 +237,17 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
             float g[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] = f[it][j] * inv;
-            dst[(int64_t)at * L] = codes8(g);
+            dst[at * L] = codes8(g);
         }
         if (lane == 0) *scale = s;
     }
 }
 
-// The queries of 64 / L heads at a time of one token, all its heads by one wave.
+// The queries of one token by one wave, 64 / L heads at a time, eight deep.
 template <int D>
 __device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
 {
-    constexpr int L = D / 8, HEADS = 64 / L;
+    constexpr int L = D / 8, HEADS = 64 / L, DEEP = 8;
     const KvCache &kc = p.c;
     const int lane = threadIdx.x & 63, c = lane % L, r = lane / L;
     const int i = find_seq(kc.cu, kc.nseq, tok, 1, 0);
@@ -250,42 +256,63 @@ __device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
     const int held = clamped(kc.seq_len[i], (int64_t)kc.table_width << kc.page_shift);
     const int64_t pos = held + (tok - c0);
     if (p.cos && pos >= p.rope_rows) return;
-    Turn t;
-    t.load(p, pos, c);
-    for (int h = 0; h < p.q_heads; h += HEADS) {
-        const bool in = h + r < p.q_heads;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (in)
-            x = *reinterpret_cast<const uint4 *>(p.src[2] + tok * p.tok_stride[2] +
-                                                 (h + r) * p.head_stride[2] + 8 * c);
-        float f[8];
-        t.apply(p, x, c, f);
-        if (in)
-            *reinterpret_cast<uint4 *>(p.q_out + tok * p.qo_tok + (h + r) * p.qo_head + 8 * c) =
-                pack8(f);
+    kvf4 cs[2] = {}, sn[2] = {};
+    if (p.cos) {
+        const int64_t at = pos * (p.rot >> 1) + turn_at(p, c);
+        cs[0] = *reinterpret_cast<const kvf4 *>(p.cos + at);
+        sn[0] = *reinterpret_cast<const kvf4 *>(p.sin + at);
+        if (!p.interleaved) {
+            cs[1] = *reinterpret_cast<const kvf4 *>(p.cos + at + 4);
+            sn[1] = *reinterpret_cast<const kvf4 *>(p.sin + at + 4);
+        }
+    }
+    const uint16_t *src = p.src[2] + tok * p.tok_stride[2] + 8 * c;
+    uint16_t *dst = p.q_out + tok * p.qo_tok + 8 * c;
+    const int last = p.q_heads - 1;
+    for (int h0 = 0; h0 < p.q_heads; h0 += DEEP * HEADS) {
+        kvu4 x[DEEP];
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int h = h0 + k * HEADS;
+            if (h <= last)
+                x[k] = *reinterpret_cast<const kvu4 *>(src + (h + r < last ? h + r : last) *
+                                                                 p.head_stride[2]);
+        }
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int h = h0 + k * HEADS;
+            if (h > last) continue;                                    // the whole wave
+            kvu4 y = x[k];
+            if (p.cos) {
+                float f[8];
+                turn(p, x[k], c, cs, sn, f);
+                y = pack8(f);
+            }
+            if (h + r <= last) *reinterpret_cast<kvu4 *>(dst + (h + r) * p.qo_head) = y;
+        }
     }
 }
 
 template <bool FP8, int D, int PAGE>
 __global__ __launch_bounds__(256) void append_kernel(KvAppendParams p)
 {
-    const int64_t unit = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
-    if (unit < p.kv_units) {
-        // neighbouring waves take the heads of one page: they read the same
-        // rows of the rotation tables
-        const int head = (int)(unit % p.c.heads);
-        const int64_t u = unit / p.c.heads;
-        append_page<FP8, D, PAGE>(p, u >> 1, head, (int)(u & 1));
-    } else if (unit - p.kv_units < p.q_units) {
-        rotate_queries<D>(p, unit - p.kv_units);
+    __shared__ __align__(16) float rope[PAGE * D];
+    int64_t b = blockIdx.x;
+    if (b < p.kv_blocks) {
+        const int quads = (p.c.heads + 3) / 4;
+        const int head = (int)(b % quads) * 4;
+        b /= quads;
+        append_page<FP8, D, PAGE>(p, b >> 1, head, (int)(b & 1), rope);
+    } else {
+        const int64_t tok = (b - p.kv_blocks) * 4 + uniform(threadIdx.x >> 6);
+        if (tok < p.N) rotate_queries<D>(p, tok);
     }
 }
 
 template <bool FP8, int D>
 hipError_t launch_page(const KvAppendParams &p, hipStream_t st)
 {
-    const int64_t blocks = (p.kv_units + p.q_units + 3) / 4;
-    if (blocks == 0) return hipSuccess;
+    const int64_t blocks = p.kv_blocks + (p.q_heads > 0 ? (p.N + 3) / 4 : 0);
     const dim3 g((uint32_t)blocks), b(256);
     switch (p.c.page_shift) {
     case 4: append_kernel<FP8, D, 16><<<g, b, 0, st>>>(p); break;
