@@ -250,6 +250,20 @@ __device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
     constexpr int L = D / 8, HEADS = 64 / L, DEEP = 8;
     const KvCache &kc = p.c;
     const int lane = threadIdx.x & 63, c = lane % L, r = lane / L;
+    const uint16_t *src = p.src[2] + tok * p.tok_stride[2] + 8 * c;
+    uint16_t *dst = p.q_out + tok * p.qo_tok + 8 * c;
+    const int last = p.q_heads - 1;
+    kvu4 x[DEEP];
+    auto load = [&](int h0) KV_INLINE {  // lanes behind the last head read it again
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int h = h0 + k * HEADS;
+            if (h <= last)
+                x[k] = *reinterpret_cast<const kvu4 *>(src + (h + r < last ? h + r : last) *
+                                                                 p.head_stride[2]);
+        }
+    };
+    load(0);                             // under way while the position is looked up
     const int i = find_seq(kc.cu, kc.nseq, tok, 1, 0);
     const int c0 = clamped(kc.cu[i], p.N), c1 = clamped(kc.cu[i + 1], p.N);
     if (tok < c0 || tok >= c1) return;                                 // rows of no sequence
@@ -266,18 +280,8 @@ __device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
             sn[1] = *reinterpret_cast<const kvf4 *>(p.sin + at + 4);
         }
     }
-    const uint16_t *src = p.src[2] + tok * p.tok_stride[2] + 8 * c;
-    uint16_t *dst = p.q_out + tok * p.qo_tok + 8 * c;
-    const int last = p.q_heads - 1;
     for (int h0 = 0; h0 < p.q_heads; h0 += DEEP * HEADS) {
-        kvu4 x[DEEP];
-#pragma unroll
-        for (int k = 0; k < DEEP; ++k) {
-            const int h = h0 + k * HEADS;
-            if (h <= last)
-                x[k] = *reinterpret_cast<const kvu4 *>(src + (h + r < last ? h + r : last) *
-                                                                 p.head_stride[2]);
-        }
+        if (h0 > 0) load(h0);
 #pragma unroll
         for (int k = 0; k < DEEP; ++k) {
             const int h = h0 + k * HEADS;
