@@ -118,22 +118,20 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
     const KvCache &kc = p.c;
     const int tid = threadIdx.x, lane = tid & 63, c = lane % L, r = lane / L;
     const int head = head0 + uniform(tid >> 6);
-    const int i = find_seq(kc.cu, kc.nseq, slot, PAGE, 2);
-    const int c0 = clamped(kc.cu[i], p.N), n = clamped(kc.cu[i + 1], p.N) - c0;
+    const Seq sq = find_seq(kc, p.N, slot, PAGE, 2);
+    const int c0 = sq.c0, n = sq.c1 - sq.c0;
     const int cap = kc.table_width * PAGE;                      // < 2^31, checked on the host
-    const int held = clamped(kc.seq_len[i], cap);
-    const int64_t pg = held / PAGE + (slot - (c0 / PAGE + 2 * (int64_t)i));
+    const int held = clamped(sq.len, cap);
+    const int64_t pg = held / PAGE + (slot - (c0 / PAGE + 2 * (int64_t)sq.i));
     // positions past the table or past the rotation's rows are not written
     int64_t end = (int64_t)held + (n > 0 ? n : 0);
     end = end < cap ? end : cap;
     if (p.cos && end > p.rope_rows) end = p.rope_rows;
     if (pg < held / PAGE || pg * PAGE >= end || held >= end) return;   // the whole block
-    const uint32_t id = (uint32_t)kc.table[(int64_t)i * kc.table_stride + pg];
-    if (id >= kc.pages) return;
+    const uint32_t id = (uint32_t)kc.table[(int64_t)sq.i * kc.table_stride + pg];
     const int s0 = pg * PAGE > held ? 0 : held - (int)pg * PAGE;       // slots to fill
     const int s1 = (int)(end - pg * PAGE < PAGE ? end - pg * PAGE : PAGE);
     const bool mine = head < kc.heads;
-    const int64_t unit = (int64_t)id * kc.heads + (mine ? head : 0);
     const int64_t ts = p.tok_stride[which];
     const uint16_t *src = p.src[which] + (mine ? head : 0) * p.head_stride[which] + 8 * c +
                           (c0 + (pg * PAGE - held)) * ts;              // slot 0's token
@@ -146,6 +144,8 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
         const int s = s0 + it * ROWS, at = s + r < s1 ? s + r : s1 - 1;
         if (s < s1) x[it] = *reinterpret_cast<const kvu4 *>(src + at * ts);
     }
+    if (id >= kc.pages) return;                                        // the whole block
+    const int64_t unit = (int64_t)id * kc.heads + (mine ? head : 0);
     const int half = p.rot >> 1;
     if (turns) {                         // the page's cosines and sines, for all its heads
         const int total = (s1 - s0) * half;
@@ -264,11 +264,10 @@ __device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
         }
     };
     load(0);                             // under way while the position is looked up
-    const int i = find_seq(kc.cu, kc.nseq, tok, 1, 0);
-    const int c0 = clamped(kc.cu[i], p.N), c1 = clamped(kc.cu[i + 1], p.N);
-    if (tok < c0 || tok >= c1) return;                                 // rows of no sequence
-    const int held = clamped(kc.seq_len[i], (int64_t)kc.table_width << kc.page_shift);
-    const int64_t pos = held + (tok - c0);
+    const Seq sq = find_seq(kc, p.N, tok, 1, 0);
+    if (tok < sq.c0 || tok >= sq.c1) return;                           // rows of no sequence
+    const int held = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
+    const int64_t pos = held + (tok - sq.c0);
     if (p.cos && pos >= p.rope_rows) return;
     kvf4 cs[2] = {}, sn[2] = {};
     if (p.cos) {

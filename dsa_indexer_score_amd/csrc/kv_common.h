@@ -87,21 +87,29 @@ __device__ inline int clamped(int x, int64_t hi)
     return x < 0 ? 0 : (int64_t)x > hi ? (int)hi : x;
 }
 
-// The largest i in [0, n) with max(cu[i], 0) / div + mul * i <= slot, by the
-// whole wave: 64 probes a step, so one load for up to 64 sequences.  For an
-// array that does not ascend the answer is some i in [0, n).
-__device__ inline int find_seq(const int32_t *cu, int n, int64_t slot, int div, int mul)
+// A sequence of the call: rows [c0, c1) of it, clamped to [0, rows], and its
+// length as given.
+struct Seq {
+    int i, c0, c1, len;
+};
+
+// The sequence of the largest i in [0, nseq) with max(cu[i], 0) / div + mul * i
+// <= slot, by the whole wave: 64 probes a step down to 64 sequences, whose
+// rows and lengths then come with one round of loads.  For an array that does
+// not ascend the answer is some sequence.
+__device__ inline Seq find_seq(const KvCache &kc, int64_t rows, int64_t slot, int div, int mul)
 {
     const int lane = threadIdx.x & 63;
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
+    int lo = 0, hi = kc.nseq;
+    auto fits = [&](int x, int i) KV_INLINE {
+        return (int64_t)((x < 0 ? 0 : x) / div) + (int64_t)mul * i <= slot;
+    };
+    while (hi - lo > 64) {
         const int step = (hi - lo + 63) / 64;
         const int64_t i = lo + (int64_t)lane * step;
         const bool in = i < hi;
         const int at = in ? (int)i : lo;
-        const int x = cu[at];
-        const bool ok = in && (int64_t)((x < 0 ? 0 : x) / div) + (int64_t)mul * at <= slot;
-        int cnt = __popcll(__ballot(ok));
+        int cnt = __popcll(__ballot(in && fits(kc.cu[at], at)));
         cnt = cnt < 1 ? 1 : cnt;
         lo += (cnt - 1) * step;
         if (lo >= hi) lo = hi - 1;
@@ -109,7 +117,17 @@ __device__ inline int find_seq(const int32_t *cu, int n, int64_t slot, int div, 
         lo = uniform(lo);
         hi = uniform(hi);
     }
-    return lo;
+    const bool in = lo + lane < hi;
+    const int at = in ? lo + lane : lo;
+    const int a = kc.cu[at], b = kc.cu[at + 1], n = kc.seq_len[at];
+    int cnt = __popcll(__ballot(in && fits(a, at)));
+    cnt = uniform(cnt < 1 ? 0 : cnt - 1);
+    Seq s;
+    s.i = lo + cnt;
+    s.c0 = clamped(__builtin_amdgcn_readlane(a, cnt), rows);
+    s.c1 = clamped(__builtin_amdgcn_readlane(b, cnt), rows);
+    s.len = __builtin_amdgcn_readlane(n, cnt);
+    return s;
 }
 
 }  // namespace

@@ -194,13 +194,13 @@ void rows_kernel(KvAttendParams p)
     const int64_t slot = p.slot0 + blk.slot;
 
     const int R = SEL ? 1 : p.tile_rows;
-    const int seq = SEL ? find_seq(kc.cu, kc.nseq, slot, 1, 0) : find_seq(kc.cu, kc.nseq, slot, R, 1);
-    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
-    const int rows_in_seq = c1 - c0;
+    const Seq sq = find_seq(kc, p.S, slot, R, SEL ? 0 : 1);
+    const int seq = sq.i, c0 = sq.c0;
+    const int rows_in_seq = sq.c1 - sq.c0;
     const int64_t t0 = SEL ? slot - c0 : (slot - (c0 / R + (int64_t)seq)) * R;
     if (t0 < 0 || t0 >= rows_in_seq) return;
     const int ntok = (int)(rows_in_seq - t0 < R ? rows_in_seq - t0 : R);
-    const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+    const int len = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
     const int64_t row0 = c0 + t0;
     // entries: keys 0 .. entries of the sequence, or of the row's selection
     int entries, base = 0;
@@ -501,14 +501,14 @@ __global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t unit = blockIdx.x;
     const int64_t row = unit / p.q_heads;
-    const int seq = find_seq(kc.cu, kc.nseq, row, 1, 0);
-    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
+    const Seq sq = find_seq(kc, p.S, row, 1, 0);
+    const int c0 = sq.c0, c1 = sq.c1;
     if (row < c0 || row >= c1) return;
     int own;
     if constexpr (SEL) {
         own = clamped(p.valid_len[row], p.W);
     } else {
-        const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+        const int len = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
         const int64_t x = p.causal ? (int64_t)len - (c1 - c0) + (row - c0) + 1 : len;
         own = x < 0 ? 0 : x < len ? (int)x : len;
     }
@@ -574,11 +574,11 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
     const KvCache &kc = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t slot = p.slot0 + blockIdx.x;
-    const int seq = find_seq(kc.cu, kc.nseq, slot, 2, 1);
-    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
+    const Seq sq = find_seq(kc, p.S, slot, 2, 1);
+    const int seq = sq.i, c0 = sq.c0, c1 = sq.c1;
     const int64_t t0 = (slot - (c0 / 2 + (int64_t)seq)) * 2;
     if (t0 < 0 || t0 >= c1 - c0) return;
-    const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+    const int len = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
     const int64_t row0 = c0 + t0;
     const bool two = t0 + 1 < c1 - c0;
     const int cnt[2] = {clamped(p.valid_len[row0], p.W), two ? clamped(p.valid_len[row0 + 1], p.W) : 0};

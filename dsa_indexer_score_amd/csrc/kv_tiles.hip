@@ -81,13 +81,13 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
     const int head = blk.head, grp = blk.grp, split = blk.split;
     const int64_t slot = p.slots - 1 - blk.slot;      // causal: the longest rows first
     const int R = p.tile_rows;
-    const int seq = find_seq(kc.cu, kc.nseq, slot, R, 1);
-    const int c0 = clamped(kc.cu[seq], p.S), c1 = clamped(kc.cu[seq + 1], p.S);
-    const int rows_in_seq = c1 - c0;
+    const Seq sq = find_seq(kc, p.S, slot, R, 1);
+    const int seq = sq.i, c0 = sq.c0;
+    const int rows_in_seq = sq.c1 - sq.c0;
     const int64_t t0 = (slot - (c0 / R + (int64_t)seq)) * R;
     if (t0 < 0 || t0 >= rows_in_seq) return;
     const int ntok = (int)(rows_in_seq - t0 < R ? rows_in_seq - t0 : R);
-    const int len = clamped(kc.seq_len[seq], (int64_t)kc.table_width << kc.page_shift);
+    const int len = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
     const int64_t row0 = c0 + t0;
     const int64_t last = p.causal ? (int64_t)len - rows_in_seq + t0 + ntok : len;
     const int entries = clamped(last < 0 ? 0 : (int)last, len);

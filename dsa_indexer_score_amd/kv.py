@@ -124,7 +124,7 @@ class KVCache:
         if Hq < 1 or Hq % self.heads:
             raise ValueError(f"q's heads must be a multiple of the cache's {self.heads}")
         if out is None:
-            o = torch.empty((S, Hq, self.d), dtype=_BF16, device=self.device)
+            o = torch.empty_like(q, memory_format=torch.contiguous_format)
             lse = torch.empty((S, Hq), dtype=torch.float32, device=self.device) if with_lse else None
         else:
             o, lse = out
@@ -182,8 +182,10 @@ class KVCache:
             rq = self._rows("q", q, rows=N)
             heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((N, heads, self.d), dtype=torch.bfloat16, device=self.device)
-            ro = self._rows("q_out", q_out, rows=N, heads=heads)
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+                ro = _lib.KvRows(q_out.data_ptr(), heads * self.d, self.d)
+            else:
+                ro = self._rows("q_out", q_out, rows=N, heads=heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
         rc = self._lib.indexer_kv_append(self._ref, seqs, rk, rv, N, _addr(cos), _addr(sin),
