@@ -32,6 +32,7 @@ struct KvAppendParams {
     int rot, interleaved;
     int q_heads;              // 0: no queries
     int64_t N;                // new tokens
+    int q_steps, q_parts;     // steps of 512 channels by a wave, waves for a token's queries
     int64_t kv_blocks;        // blocks of pages, before those of queries
 };
 

@@ -115,6 +115,7 @@ struct Plan {
 // rows of up to 16,384 keys: 258 us with parts of 4,096, 272 with 8,192, 264
 // with 2,048.
 constexpr int64_t kFillBlocks = 512;
+constexpr int64_t kFillWaves = 4096;
 constexpr int64_t kMinChunk = 512;
 constexpr int64_t kRaggedChunk = 4096;
 // Columns (query rows of a sequence x query heads of a key head) up to which a
@@ -317,7 +318,14 @@ int indexer_kv_append(const indexer_kv_cache *c, const indexer_kv_seqs *s,
     // A sequence of n new tokens touches at most n / page + 2 pages; with
     // page slots numbered from cu / page + 2 i, sequence i has that many.
     p.kv_blocks = (N / c->page + 2 * (int64_t)s->nseq) * div_up(c->heads, 4) * 2;
-    if (p.kv_blocks + N >= INT32_MAX) return IDX_EUNSUPPORTED;
+    // A wave turns up to eight steps of 512 / d heads of a token's queries; a few
+    // tokens are spread over more waves (64 tokens x 64 heads: 9.7 us by 16
+    // steps in one wave, 5.4 by one step each).
+    const int64_t steps = div_up(q_heads, 512 / c->d);
+    p.q_steps = 8;
+    while (p.q_steps > 1 && N * div_up(steps, p.q_steps) < kFillWaves) p.q_steps /= 2;
+    p.q_parts = (int)std::max<int64_t>(1, div_up(steps, p.q_steps));
+    if (p.kv_blocks + N * p.q_parts >= INT32_MAX) return IDX_EUNSUPPORTED;
     DeviceGuard guard(c->device);
     if (guard.err != hipSuccess) return fail_hip(guard.err);
     const hipError_t e = dsai::launch_kv_append(c->dtype, c->d, p, static_cast<hipStream_t>(stream));

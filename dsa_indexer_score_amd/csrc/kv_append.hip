@@ -144,15 +144,29 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
         const int s = s0 + it * ROWS, at = s + r < s1 ? s + r : s1 - 1;
         if (s < s1) x[it] = *reinterpret_cast<const kvu4 *>(src + at * ts);
     }
+    // the page's cosines and sines, for all its heads: the first round of loads
+    // as well, before anything waits for the page id
+    const int half = p.rot >> 1;
+    const int total = turns ? (s1 - s0) * half : 0;
+    const float *cos = p.cos + (pg * PAGE + s0) * half, *sin = p.sin + (pg * PAGE + s0) * half;
+    kvf4 cs0 = {}, sn0 = {};
+    if (4 * tid < total) {
+        cs0 = *reinterpret_cast<const kvf4 *>(cos + 4 * tid);
+        sn0 = *reinterpret_cast<const kvf4 *>(sin + 4 * tid);
+    }
     if (id >= kc.pages) return;                                        // the whole block
     const int64_t unit = (int64_t)id * kc.heads + (mine ? head : 0);
-    const int half = p.rot >> 1;
-    if (turns) {                         // the page's cosines and sines, for all its heads
-        const int total = (s1 - s0) * half;
-        const float *cs = p.cos + (pg * PAGE + s0) * half, *sn = p.sin + (pg * PAGE + s0) * half;
-        for (int k = 4 * tid; k < total; k += 1024) {
-            *reinterpret_cast<kvf4 *>(rope + k) = *reinterpret_cast<const kvf4 *>(cs + k);
-            *reinterpret_cast<kvf4 *>(rope + total + k) = *reinterpret_cast<const kvf4 *>(sn + k);
+    float old = 0.0f;                    // the scale of a page that holds tokens already
+    if constexpr (FP8)
+        if (s0 > 0) old = (which ? kc.v_scale : kc.k_scale)[unit];
+    if (turns) {
+        if (4 * tid < total) {
+            *reinterpret_cast<kvf4 *>(rope + 4 * tid) = cs0;
+            *reinterpret_cast<kvf4 *>(rope + total + 4 * tid) = sn0;
+        }
+        for (int k = 4 * tid + 1024; k < total; k += 1024) {
+            *reinterpret_cast<kvf4 *>(rope + k) = *reinterpret_cast<const kvf4 *>(cos + k);
+            *reinterpret_cast<kvf4 *>(rope + total + k) = *reinterpret_cast<const kvf4 *>(sin + k);
         }
         __syncthreads();
         rope += turn_at(p, c);
@@ -207,7 +221,6 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
         uint2 *dst = reinterpret_cast<uint2 *>(which ? kc.v : kc.k) + unit * PAGE * L + c;
         float s = pow2_scale(amax);
         if (s0 > 0) {
-            const float old = *scale;
             if (old >= s) {
                 s = old;
             } else {                                                   // the held tokens' codes
@@ -243,27 +256,29 @@ __device__ inline void append_page(const KvAppendParams &p, int64_t slot, int he
     }
 }
 
-// The queries of one token by one wave, 64 / L heads at a time, eight deep.
+// The queries of one token, p.q_steps steps of 64 / L heads by one wave, up to
+// eight loads deep.
 template <int D>
-__device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
+__device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok, int part)
 {
     constexpr int L = D / 8, HEADS = 64 / L, DEEP = 8;
     const KvCache &kc = p.c;
     const int lane = threadIdx.x & 63, c = lane % L, r = lane / L;
     const uint16_t *src = p.src[2] + tok * p.tok_stride[2] + 8 * c;
     uint16_t *dst = p.q_out + tok * p.qo_tok + 8 * c;
-    const int last = p.q_heads - 1;
+    const int last = p.q_heads - 1, first = part * p.q_steps * HEADS;
+    const int end = first + p.q_steps * HEADS <= last ? first + p.q_steps * HEADS : last + 1;
     kvu4 x[DEEP];
     auto load = [&](int h0) KV_INLINE {  // lanes behind the last head read it again
 #pragma unroll
         for (int k = 0; k < DEEP; ++k) {
             const int h = h0 + k * HEADS;
-            if (h <= last)
+            if (h < end)
                 x[k] = *reinterpret_cast<const kvu4 *>(src + (h + r < last ? h + r : last) *
                                                                  p.head_stride[2]);
         }
     };
-    load(0);                             // under way while the position is looked up
+    load(first);                         // under way while the position is looked up
     const Seq sq = find_seq(kc, p.N, tok, 1, 0);
     if (tok < sq.c0 || tok >= sq.c1) return;                           // rows of no sequence
     const int held = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
@@ -279,12 +294,12 @@ __device__ inline void rotate_queries(const KvAppendParams &p, int64_t tok)
             sn[1] = *reinterpret_cast<const kvf4 *>(p.sin + at + 4);
         }
     }
-    for (int h0 = 0; h0 < p.q_heads; h0 += DEEP * HEADS) {
-        if (h0 > 0) load(h0);
+    for (int h0 = first; h0 < end; h0 += DEEP * HEADS) {
+        if (h0 > first) load(h0);
 #pragma unroll
         for (int k = 0; k < DEEP; ++k) {
             const int h = h0 + k * HEADS;
-            if (h > last) continue;                                    // the whole wave
+            if (h >= end) continue;                                    // the whole wave
             kvu4 y = x[k];
             if (p.cos) {
                 float f[8];
@@ -307,15 +322,16 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppendParams p)
         b /= quads;
         append_page<FP8, D, PAGE>(p, b >> 1, head, (int)(b & 1), rope);
     } else {
-        const int64_t tok = (b - p.kv_blocks) * 4 + uniform(threadIdx.x >> 6);
-        if (tok < p.N) rotate_queries<D>(p, tok);
+        const uint32_t u = (uint32_t)(b - p.kv_blocks) * 4 + uniform(threadIdx.x >> 6);
+        const uint32_t tok = u / (uint32_t)p.q_parts;
+        if (tok < p.N) rotate_queries<D>(p, tok, (int)(u % (uint32_t)p.q_parts));
     }
 }
 
 template <bool FP8, int D>
 hipError_t launch_page(const KvAppendParams &p, hipStream_t st)
 {
-    const int64_t blocks = p.kv_blocks + (p.q_heads > 0 ? (p.N + 3) / 4 : 0);
+    const int64_t blocks = p.kv_blocks + (p.q_heads > 0 ? (p.N * p.q_parts + 3) / 4 : 0);
     const dim3 g((uint32_t)blocks), b(256);
     switch (p.c.page_shift) {
     case 4: append_kernel<FP8, D, 16><<<g, b, 0, st>>>(p); break;
