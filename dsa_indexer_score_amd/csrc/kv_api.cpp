@@ -111,12 +111,13 @@ struct Plan {
 // Two blocks for each CU: 262,144 keys, 8 key heads, one row take 105 us with
 // 512 blocks, 111 with 768.  A part below 512 keys costs more in the join than
 // it saves (4 rows of 517 keys: 11.3 against 15.7 us a call with parts of 256;
-// 16 rows of 2,048 selected keys 28.4 against 37.5 with parts of 1,024).  64
+// 16 rows of 2,048 selected keys, whose looking up takes longer: 16.8 us with
+// parts of 256, 17.2 with 512).  64
 // rows of up to 16,384 keys: 258 us with parts of 4,096, 272 with 8,192, 264
 // with 2,048.
 constexpr int64_t kFillBlocks = 512;
 constexpr int64_t kFillWaves = 4096;
-constexpr int64_t kMinChunk = 512;
+constexpr int64_t kMinChunk = 512, kMinPicked = 256;
 constexpr int64_t kRaggedChunk = 4096;
 // Columns (query rows of a sequence x query heads of a key head) up to which a
 // sequence's rows go by blocks of 32 columns, straight from memory.
@@ -167,7 +168,7 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
     // does not trail the others
     const int64_t keys = std::max<int64_t>(max_len, 1);
     const int64_t fill = (p.tiles ? kFillTiles : kFillBlocks) / units;
-    int64_t nsplit = std::min(fill, keys / (p.tiles ? kMinTileChunk : kMinChunk));
+    int64_t nsplit = std::min(fill, keys / (p.tiles ? kMinTileChunk : selected ? kMinPicked : kMinChunk));
     if (!p.tiles && !selected && nseq > 1) nsplit = std::max(nsplit, keys / kRaggedChunk);
     nsplit = std::max<int64_t>(nsplit, 1);
     int64_t chunk = round_up(div_up(keys, nsplit), 128);
