@@ -133,7 +133,12 @@ def test_workspace_is_asked_for_exactly_when_rows_are_split():
         assert size(wide, *bad)[0] == _lib.IDX_EINVAL
     sel = lambda S, W: (lib.indexer_kv_attend_selected_workspace_bytes(  # noqa: E731
         cache(), wide, S, 16, W, ctypes.byref(n)), n.value)
-    assert sel(4096, 2048) == (0, 0) and sel(1, 200) == (0, 0)
+    assert sel(1, 200) == (0, 0) and sel(4096, 5000) == (0, 0)
+    # many rows: lists of two rows' positions (2 W entries and their counts), at
+    # most 256 MB of them at a time
+    pairs = 4096 // 2 + 1
+    assert sel(4096, 2048) == (0, pairs * (2 * 2048 * 4 + 16))
+    assert sel(10 ** 6, 2048)[1] <= 2 ** 28 < sel(10 ** 6, 2048)[1] + 2 * 2048 * 4 + 16 + 256
     rc, few = sel(1, 2048)
     assert rc == 0 and few > 0
     assert selected(s=wide, S=1, q_heads=16, W=2048) == _lib.IDX_EWORKSPACE
