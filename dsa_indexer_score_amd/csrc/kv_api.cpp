@@ -80,6 +80,18 @@ bool rows_apart(const indexer_kv_rows *r, int64_t rows, int64_t heads, int64_t d
            (r->row_stride >= d && r->head_stride >= (rows - 1) * r->row_stride + d);
 }
 
+// Bytes from the first element of a rows tensor to behind its last.
+uintptr_t span(const indexer_kv_rows *r, int64_t rows, int64_t heads, int64_t d)
+{
+    return (uintptr_t)((rows - 1) * r->row_stride + (heads - 1) * r->head_stride + d) * 2;
+}
+
+bool overlap(const void *a, uintptr_t an, const void *b, uintptr_t bn)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
 dsai::KvCache kernel_cache(const indexer_kv_cache *c, const indexer_kv_seqs *s)
 {
     dsai::KvCache k{};
@@ -210,9 +222,12 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     if (rc != IDX_OK) return rc;
     rc = check_seqs(c, s, S);
     if (rc != IDX_OK) return rc;
-    if (!std::isfinite(scale)) return IDX_EINVAL;
+    const double c2 = std::fabs((double)scale) * 1.4426950408889634074;
+    if (!std::isfinite((float)c2)) return IDX_EINVAL;
     if (S == 0 || s->nseq == 0) return IDX_OK;  // no row belongs to a sequence
     if (!rows_ok(q) || !out || !aligned(out, 16) || !aligned(lse, 4)) return IDX_EINVAL;
+    if (overlap(q->ptr, span(q, S, q_heads, c->d), out, (uintptr_t)S * q_heads * c->d * 2))
+        return IDX_EINVAL;  // blocks read rows that others may have written
     const Plan pl = make_plan(c, S, q_heads, s->nseq, idx ? W : most_keys(c, s, max_len),
                               idx != nullptr);
     if ((pl.slots * pl.nsplit * c->heads + 8) * pl.groups >= INT32_MAX) return IDX_EUNSUPPORTED;
@@ -229,7 +244,7 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     p.S = S;
     p.q_heads = q_heads;
     p.group = q_heads / c->heads;
-    p.c2 = (float)(std::fabs((double)scale) * 1.4426950408889634074);
+    p.c2 = (float)c2;
     p.q_and = 0xffffffffu;
     p.q_xor = scale < 0.0f ? 0x80008000u : 0;
     if (p.c2 == 0.0f) p.c2 = 1.0f, p.q_and = 0;
@@ -294,6 +309,11 @@ int indexer_kv_append(const indexer_kv_cache *c, const indexer_kv_seqs *s,
     if (!rows_ok(k) || !rows_ok(v)) return IDX_EINVAL;
     if (q_heads > 0 && (!rows_ok(q) || !rows_ok(q_out) || !rows_apart(q_out, N, q_heads, c->d)))
         return IDX_EINVAL;
+    if (q_heads > 0 &&
+        (q->ptr != q_out->ptr || (N > 1 && q->row_stride != q_out->row_stride) ||
+         (q_heads > 1 && q->head_stride != q_out->head_stride)) &&
+        overlap(q->ptr, span(q, N, q_heads, c->d), q_out->ptr, span(q_out, N, q_heads, c->d)))
+        return IDX_EINVAL;  // in place is fine, anything between is not
 
     dsai::KvAppendParams p{};
     p.c = kernel_cache(c, s);

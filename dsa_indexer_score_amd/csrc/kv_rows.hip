@@ -581,7 +581,9 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
     const int len = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
     const int64_t row0 = c0 + t0;
     const bool two = t0 + 1 < c1 - c0;
-    const int cnt[2] = {clamped(p.valid_len[row0], p.W), two ? clamped(p.valid_len[row0 + 1], p.W) : 0};
+    const int most = len > 0 ? p.W : 0;   // no token: nothing to look up
+    const int cnt[2] = {clamped(p.valid_len[row0], most),
+                        two ? clamped(p.valid_len[row0 + 1], most) : 0};
     const int base = p.idx0 ? p.idx0[seq] : 0;
     const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
 

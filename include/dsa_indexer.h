@@ -473,8 +473,8 @@ typedef struct {
  *   interleaved  1: pair j is channels 2j and 2j + 1; 0: j and j + rot / 2.
  *   q, q_heads, q_out  bf16 [N, q_heads, d]: the new tokens' queries, turned
  *             the same way into q_out (rounded to nearest even; may be q
- *             itself, may not overlap it otherwise); q_heads = 0: none.  The
- *             rows of q_out must not overlap: one of its strides spans the
+ *             itself, may not overlap it otherwise: IDX_EINVAL); q_heads = 0:
+ *             none.  The rows of q_out must not overlap: one of its strides spans the
  *             whole of the other (IDX_EINVAL).
  * Positions at or past table_width * page or (with a rotation) rope_rows are
  * not written, nor are their queries when past rope_rows.
@@ -503,12 +503,13 @@ int indexer_kv_append(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs
  * it sees all seq_len[i] of them.
  *   q         bf16 [S, q_heads, d]; q_heads a multiple of the cache's heads,
  *             query head h reads key head h / (q_heads / heads).
- *   scale     factor of the scores, finite.
+ *   scale     factor of the scores, finite (as scale * log2 e).
  *   max_len   host, an upper bound on seq_len (0 = unknown: table_width *
  *             page); sizes the split along the keys and the workspace.  A
  *             longer sequence breaks the precondition: its rows' results are
  *             unspecified, every access stays in bounds.
- *   out       device bf16 [S, q_heads, d], contiguous, 16-byte aligned.
+ *   out       device bf16 [S, q_heads, d], contiguous, 16-byte aligned; may not
+ *             overlap q (IDX_EINVAL).
  *   lse       device fp32 [S, q_heads] or NULL.
  *   workspace device, 16-byte aligned, of at least
  *             indexer_kv_attend_workspace_bytes(...) bytes for the same sizes

@@ -199,6 +199,122 @@ def test_attend_reads_strided_queries():
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("nseq", [130, 4500])
+def test_more_sequences_than_one_round_of_probes(nseq):
+    """Sequences of 0 to 40 tokens with 0 to 3 rows, some without rows at all:
+    attention, selected attention and append find every row's sequence."""
+    g = np.random.default_rng(nseq)
+    lens = g.integers(1, 40, nseq)
+    rows = np.minimum(g.integers(0, 4, nseq), lens)
+    pr = Problem(nseq, FP8, 1, 64, 16, list(lens), nan=False, pow2=True)
+    S = int(rows.sum())
+    cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    q = pr.queries(S, 2)
+    cache = pr.gpu()
+    args = dev(cu), dev(pr.lens), dev(pr.table)
+    ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
+                     pr.cache["v"], pr.scale["v"], 0.125)
+    out, lse = cache.attend(q.to(DEV), *args, with_lse=True)
+    check(out, lse, ref, 64, "all")
+    idx, vl = selection(g, S, 33, cu, [int(x) for x in lens])
+    ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
+                     pr.cache["v"], pr.scale["v"], 0.125, idx=idx, valid_len=vl)
+    out, lse = cache.attend_selected(q.to(DEV), dev(idx), dev(vl), *args, with_lse=True)
+    check(out, lse, ref, 64, "selected")
+    # the rows' tokens again, behind what precedes them
+    x = torch.from_numpy(g.standard_normal((S, 1, 64)).astype(np.float32)).to(BF16)
+    held = (lens - rows).astype(np.int32)
+    want, s = okv.append(pr.cache["k"], pr.scale["k"], x.float().numpy(), cu, held, pr.table)
+    cache.append(x.to(DEV), x.to(DEV), dev(cu), dev(held), dev(pr.table))
+    assert np.array_equal(cache.k.view(torch.uint8).cpu().numpy(), want)
+    assert np.array_equal(cache.k_scale.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("dtype", [FP8, BF16])
+def test_rows_past_four_gigabytes(dtype):
+    """Pages at the end of buffers of 2^32 bytes and more, by every path."""
+    H, d, page = 2, 128, 128
+    each = H * page * d * (1 if dtype == FP8 else 2)
+    pages = 2 ** 32 // each + 40
+    cache = dsai.KVCache.allocate(pages, H, d, page=page, dtype=dtype, device=DEV)
+    assert cache.k.numel() * cache.k.element_size() > 2 ** 32
+    L, n, G = 1200, 300, 4
+    ids = (pages - 1 - np.random.default_rng(1).permutation(39)[:10]).astype(np.int32)[None]
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn((L, H, d), generator=g, device=DEV).to(BF16) for _ in range(2))
+    q = torch.randn((n, H * G, d), generator=g, device=DEV).to(BF16)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    cache.append(k, v, i32(0, L), i32(0), dev(ids))
+    # a small cache with the same pages
+    twin = dsai.KVCache.allocate(10, H, d, page=page, dtype=dtype, device=DEV)
+    low = torch.arange(10, dtype=torch.int32, device=DEV)[None]
+    twin.append(k, v, i32(0, L), i32(0), low)
+    at = dev(ids[0]).long()
+    for w in ("k", "v"):
+        a, b = getattr(cache, w), getattr(twin, w)
+        filled = L // page
+        assert torch.equal(a[at[:filled]].view(torch.uint8), b[:filled].view(torch.uint8))
+    idx = torch.arange(0, L, 5, dtype=torch.int32, device=DEV).repeat(n, 1)
+    vl = torch.full((n,), idx.shape[1], dtype=torch.int32, device=DEV)
+    for rows, name in ((1, "one row"), (n, "many rows")):
+        cu = i32(0, rows)
+        a = cache.attend(q[:rows], cu, i32(L), dev(ids), with_lse=True)
+        b = twin.attend(q[:rows], cu, i32(L), low, with_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), name
+        a = cache.attend_selected(q[:rows], idx[:rows], vl[:rows], cu, i32(L), dev(ids), with_lse=True)
+        b = twin.attend_selected(q[:rows], idx[:rows], vl[:rows], cu, i32(L), low, with_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), name
+    check(*twin.attend(q, i32(0, n), i32(L), low, with_lse=True), okv.attend(
+        q.double().cpu().numpy(), [0, n], [L], low.cpu().numpy(),
+        twin.k.view(torch.uint8).cpu().numpy() if dtype == FP8 else twin.k.float().cpu().numpy(),
+        None if dtype == BF16 else twin.k_scale.cpu().numpy(),
+        twin.v.view(torch.uint8).cpu().numpy() if dtype == FP8 else twin.v.float().cpu().numpy(),
+        None if dtype == BF16 else twin.v_scale.cpu().numpy(), d ** -0.5), d, "twin")
+
+
+def test_pair_lists_of_more_than_one_launch():
+    """More rows than the lists of one launch hold: the rows behind it as well."""
+    S, W, L = 17001, 4096, 200
+    pr = Problem(3, FP8, 1, 64, 16, [L], pow2=True)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    idx = torch.full((S, W), -1, dtype=torch.int32, device=DEV)
+    idx[:, :40] = torch.rand((S, L), generator=g, device=DEV).argsort(1)[:, :40].sort(1).values.int()
+    vl = torch.randint(1, 41, (S,), generator=g, device=DEV).int()
+    q = torch.randn((S, 1, 64), generator=g, device=DEV).to(BF16)
+    cache = pr.gpu()
+    args = dev(np.array([0, S], np.int32)), dev(pr.lens), dev(pr.table)
+    assert cache.attend_selected_workspace_bytes(S, 1, 1, W) <= 2 ** 28
+    out, lse = cache.attend_selected(q, idx, vl, *args, with_lse=True)
+    K, _ = okv.sequence(pr.cache["k"], pr.scale["k"], pr.table[0], L)
+    V, _ = okv.sequence(pr.cache["v"], pr.scale["v"], pr.table[0], L)
+    at = idx[:, :40].long()
+    x = (q.double() * torch.from_numpy(K[:, 0]).to(DEV)[at]).sum(2) * 64 ** -0.5
+    x.masked_fill_(torch.arange(40, device=DEV) >= vl[:, None], -float("inf"))
+    p, val = x.softmax(1), torch.from_numpy(V[:, 0]).to(DEV)[at]
+    ref = (p[:, :, None] * val).sum(1).cpu().numpy()[:, None]
+    mag = (p[:, :, None] * val.abs()).sum(1).cpu().numpy()[:, None]
+    size = (q.double().abs() * torch.from_numpy(np.abs(K[:, 0])).to(DEV)[at]).sum(2).amax(1)
+    check(out, lse, (ref, x.logsumexp(1).cpu().numpy()[:, None], mag,
+                     size.cpu().numpy()[:, None] * 64 ** -0.5, vl.cpu().numpy()), 64, "pairs")
+
+
+def test_a_table_of_no_width_holds_nothing():
+    cache = dsai.KVCache.allocate(4, 1, 64, page=16, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    for S in (1, 200, 1100):
+        q = torch.randn((S, 1, 64), device=DEV).to(BF16)
+        args = i32(0, S), i32(50), torch.empty((1, 0), dtype=torch.int32, device=DEV)
+        out, lse = cache.attend(q, *args, with_lse=True)
+        assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+        idx = torch.arange(7, dtype=torch.int32, device=DEV).repeat(S, 1)
+        out, lse = cache.attend_selected(q, idx, torch.full((S,), 7, dtype=torch.int32, device=DEV),
+                                         *args, with_lse=True)
+        assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+        before = cache.k.view(torch.uint8).clone()
+        cache.append(q, q, *args)
+        assert torch.equal(before, cache.k.view(torch.uint8))
+
+
 @pytest.mark.parametrize("group", [4, 64])
 @pytest.mark.parametrize("dtype", [FP8, BF16])
 def test_pages_that_do_not_exist_are_masked(dtype, group):

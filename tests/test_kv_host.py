@@ -11,7 +11,8 @@ from dsa_indexer_score_amd import _lib
 from dsa_indexer_score_amd.kv import KVCache
 from oracle import kv as okv
 
-P = 1 << 20          # a pointer that is never followed: 16-byte aligned
+P = 1 << 20          # pointers that are never followed: 16-byte aligned
+OUT = P + (1 << 40)
 
 
 def cache(**kw):
@@ -52,14 +53,14 @@ BAD_SEQS = [
 ]
 
 
-def attend(c=None, s=None, q=None, S=5, q_heads=8, scale=0.1, causal=1, max_len=0, out=P, lse=P,
+def attend(c=None, s=None, q=None, S=5, q_heads=8, scale=0.1, causal=1, max_len=0, out=OUT, lse=P,
            ws=None, n=0):
     return _lib.load().indexer_kv_attend(c or cache(), s or seqs(), q or rows(), S, q_heads, scale,
                                          causal, max_len, out, lse, ws, n, None)
 
 
 def selected(c=None, s=None, q=None, S=5, q_heads=8, scale=0.1, idx=P, W=9, vl=P, idx0=None,
-             out=P, lse=P, ws=None, n=0):
+             out=OUT, lse=P, ws=None, n=0):
     return _lib.load().indexer_kv_attend_selected(c or cache(), s or seqs(), q or rows(), S,
                                                   q_heads, scale, idx, W, vl, idx0, out, lse, ws,
                                                   n, None)
@@ -83,7 +84,7 @@ def test_bad_caches_and_sequences_are_refused(call):
 def test_bad_arguments_of_attend_are_refused():
     for fn in (attend, selected):
         for kw in (dict(S=-1), dict(q_heads=0), dict(q_heads=7), dict(scale=float("inf")),
-                   dict(scale=float("nan")), dict(out=None), dict(out=P + 2), dict(lse=P + 2),
+                   dict(scale=float("nan")), dict(scale=3e38), dict(out=None), dict(out=P + 2), dict(lse=P + 2),
                    dict(q=rows(P + 8)), dict(q=rows(None)), dict(q=rows(row_stride=130)),
                    dict(q=rows(head_stride=-128)), dict(q=rows(row_stride=-256))):
             assert fn(**kw) == _lib.IDX_EINVAL, kw
@@ -93,6 +94,17 @@ def test_bad_arguments_of_attend_are_refused():
         assert attend(**kw) == _lib.IDX_EINVAL
     for kw in (dict(W=0), dict(idx=None), dict(vl=None), dict(idx=P + 2), dict(idx0=P + 1)):
         assert selected(**kw) == _lib.IDX_EINVAL
+
+
+def test_outputs_that_overlap_the_queries_are_refused():
+    """q of 5 rows, 256 elements apart, 8 heads 128 apart: 2,304 elements from first to last."""
+    far = P + 2 * (4 * 256 + 7 * 128 + 128)
+    for fn in (attend, selected):
+        for out in (P, P + 16, far - 16, P - 2 * 5 * 8 * 128 + 16):
+            assert fn(out=out) == _lib.IDX_EINVAL, out
+    ok = dict(q=rows(), q_heads=2)
+    for q_out in (rows(P + 16), rows(P, 512, 128), rows(P, 256, 1280), rows(P + 2 * 4 * 256)):
+        assert append(q_out=q_out, **ok) == _lib.IDX_EINVAL
 
 
 def test_bad_arguments_of_append_are_refused():
