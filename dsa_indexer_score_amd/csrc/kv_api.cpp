@@ -138,7 +138,7 @@ constexpr int kTilesHeads = 64;       // query heads of a key head in a block of
 // Lists of one launch's pairs: 256 MB, about 16,000 pairs of 2,048 positions;
 // more rows take several launches.
 constexpr int64_t kPickBytes = int64_t(1) << 28;
-constexpr int64_t kFillTiles = 256;   // blocks of eight waves, one for each CU
+constexpr int64_t kCus = 256;
 constexpr int64_t kMinTileChunk = 512;
 
 Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int64_t max_len,
@@ -175,13 +175,26 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
         p.bytes = p.part_ml + p.pass * 16;
         return p;
     }
-    // parts that fill the GPU, as far as they are worth a block each; among
-    // several sequences parts of at most kRaggedChunk keys, so that the longest
-    // does not trail the others
     const int64_t keys = std::max<int64_t>(max_len, 1);
-    const int64_t fill = (p.tiles ? kFillTiles : kFillBlocks) / units;
-    int64_t nsplit = std::min(fill, keys / (p.tiles ? kMinTileChunk : selected ? kMinPicked : kMinChunk));
-    if (!p.tiles && !selected && nseq > 1) nsplit = std::max(nsplit, keys / kRaggedChunk);
+    int64_t nsplit;
+    if (p.tiles) {
+        // The longest block should not outlast the others: parts of at most a
+        // CU's share, less where two blocks run on a CU (d = 64), with rows that
+        // are a sequence's last ones and see half of themselves on average.  One
+        // prompt of 4,001 tokens (d = 64, 12 / 4 heads): 120 us in one part, 79 in
+        // four; 4,096 rows over 16,384 keys (d = 128, 16 / 4 heads, as many blocks
+        // as CUs): 580 in one, 617 in two.
+        const int64_t seen = keys - std::min(rows, keys) / 2;
+        const int64_t share = std::max<int64_t>(
+            units * seen / kCus * (c->d == 64 ? 3 : 5) / 4, 1);
+        nsplit = std::min(div_up(keys, share), keys / kMinTileChunk);
+    } else {
+        // parts that fill the GPU, as far as they are worth a block each; among
+        // several sequences parts of at most kRaggedChunk keys, so that the
+        // longest does not trail the others
+        nsplit = std::min(kFillBlocks / units, keys / (selected ? kMinPicked : kMinChunk));
+        if (!selected && nseq > 1) nsplit = std::max(nsplit, keys / kRaggedChunk);
+    }
     nsplit = std::max<int64_t>(nsplit, 1);
     int64_t chunk = round_up(div_up(keys, nsplit), 128);
     nsplit = div_up(keys, chunk);

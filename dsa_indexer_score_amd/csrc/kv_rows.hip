@@ -12,8 +12,8 @@
 // waves take turns at tiles of 32 keys, each with a softmax state of its own,
 // joined through LDS at the end.  Nothing but the list of key rows is shared in
 // the loop, so there is no barrier in it: keys and values go from memory through
-// registers and a part of LDS of the wave's own to the matrix unit.  Both products are computed
-// transposed, S^T = K Q^T and O^T = V^T P^T:
+// registers and a part of LDS of the wave's own to the matrix unit.  Both
+// products are computed transposed, S^T = K Q^T and O^T = V^T P^T:
 //  - the keys are the rows of A; lane (m, g) reads 16-byte chunks of key m, and
 //    the contraction takes the channels in the order in which they come;
 //  - S^T leaves lane (n, g) with the scores of column n against keys 4 g + i of
@@ -23,7 +23,7 @@
 //    LDS reads (ds_read_b64_tr_b8, _b16) give them; codes are widened exactly to
 //    bf16.
 // P is rounded to bf16 for the matrix unit after it took the value page's scale
-// (relative 2^-9, as the rounding of the output); l sums the unrounded
+// (relative 2^-8, as the rounding of the output); l sums the unrounded
 // probabilities.
 //
 // Blocks that share a row (more keys than one chunk) write (o, m, l) to the
