@@ -43,13 +43,17 @@ int check_cache(const indexer_kv_cache *c)
     return IDX_OK;
 }
 
+// Positions, and entries of a row, that a call may count: the kernels' loops run
+// up to 2^17 past the last one in 32 bits.
+constexpr int64_t kMaxKeys = (int64_t(1) << 31) - (int64_t(1) << 18);
+
 // Sizes only: what the workspace functions may look at.
 int check_seq_sizes(const indexer_kv_cache *c, const indexer_kv_seqs *s, int64_t rows)
 {
     if (!s || s->nseq < 0 || s->table_width < 0 || rows < 0) return IDX_EINVAL;
     if (s->nseq > 0 && s->table_stride < s->table_width) return IDX_EINVAL;
     if (rows + 2 * (int64_t)s->nseq >= INT32_MAX ||
-        (int64_t)s->table_width * c->page >= INT32_MAX)
+        (int64_t)s->table_width * c->page >= kMaxKeys)
         return IDX_EUNSUPPORTED;
     return IDX_OK;
 }
@@ -238,9 +242,14 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     const double c2 = std::fabs((double)scale) * 1.4426950408889634074;
     if (!std::isfinite((float)c2)) return IDX_EINVAL;
     if (S == 0 || s->nseq == 0) return IDX_OK;  // no row belongs to a sequence
+    if (idx && W >= kMaxKeys) return IDX_EUNSUPPORTED;
     if (!rows_ok(q) || !out || !aligned(out, 16) || !aligned(lse, 4)) return IDX_EINVAL;
-    if (overlap(q->ptr, span(q, S, q_heads, c->d), out, (uintptr_t)S * q_heads * c->d * 2))
-        return IDX_EINVAL;  // blocks read rows that others may have written
+    // blocks read rows when others have written theirs
+    const uintptr_t qn = span(q, S, q_heads, c->d), ln = lse ? (uintptr_t)S * q_heads * 4 : 0;
+    const uintptr_t on = (uintptr_t)S * q_heads * c->d * 2;
+    if (overlap(q->ptr, qn, out, on) || (lse && overlap(q->ptr, qn, lse, ln)) ||
+        (lse && overlap(out, on, lse, ln)))
+        return IDX_EINVAL;
     const Plan pl = make_plan(c, S, q_heads, s->nseq, idx ? W : most_keys(c, s, max_len),
                               idx != nullptr);
     if ((pl.slots * pl.nsplit * c->heads + 8) * pl.groups >= INT32_MAX) return IDX_EUNSUPPORTED;
@@ -394,6 +403,7 @@ int indexer_kv_attend_selected_workspace_bytes(const indexer_kv_cache *c, const 
     if (!bytes || W < 1) return IDX_EINVAL;
     const int rc = check_attend_sizes(c, s, S, q_heads);
     if (rc != IDX_OK) return rc;
+    if (W >= kMaxKeys) return IDX_EUNSUPPORTED;
     *bytes = S > 0 && s->nseq > 0 ? (size_t)make_plan(c, S, q_heads, s->nseq, W, true).bytes : 0;
     return IDX_OK;
 }
@@ -404,7 +414,8 @@ int indexer_kv_attend_selected(const indexer_kv_cache *c, const indexer_kv_seqs 
                                const int32_t *idx0, void *out, float *lse, void *workspace,
                                size_t workspace_bytes, void *stream)
 {
-    if (W < 1 || !idx || !valid_len || !aligned(idx, 4) || !aligned(valid_len, 4) ||
+    const bool none = S == 0 || (s && s->nseq == 0);    // no rows to select for
+    if (W < 1 || (!none && (!idx || !valid_len)) || !aligned(idx, 4) || !aligned(valid_len, 4) ||
         !aligned(idx0, 4))
         return IDX_EINVAL;
     return attend(c, s, q, S, q_heads, scale, 0, 0, idx, W, valid_len, idx0, out, lse, workspace,

@@ -513,7 +513,7 @@ __global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
         own = x < 0 ? 0 : x < len ? (int)x : len;
     }
     if (own <= p.chunk) return;                     // written by its one block
-    int parts = (own + p.chunk - 1) / p.chunk;
+    int parts = (own - 1) / p.chunk + 1;            // own + chunk may pass 32 bits
     parts = parts < p.nsplit ? parts : p.nsplit;
     const int64_t step = p.S * p.q_heads;
     float m = -__builtin_inff();

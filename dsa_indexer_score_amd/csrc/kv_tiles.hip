@@ -261,7 +261,8 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
             }
         }
         if (st < 4) {
-            sm_ks[buf][st] = gone ? -1.0f : FP8 ? sc * p.c2 : p.c2;
+            // normal and so above 0: it multiplies the -inf of what is masked
+            sm_ks[buf][st] = gone ? -1.0f : fmaxf(FP8 ? sc * p.c2 : p.c2, 0x1p-126f);
         }
     };
     // values: wave gw takes keys 16 gw .. 16 gw + 15, lane (dq, half): channels

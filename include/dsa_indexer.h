@@ -426,7 +426,7 @@ int indexer_screen_certificates(indexer_t h, const void *q, const float *q_scale
  *             table_stride, entry j for positions [j * page, (j + 1) * page);
  *             entries past the sequence's last page may hold anything.
  *   table_width  entries that may be read of a row (table_width * page <
- *             2^31); seq_len above table_width * page is taken as that.
+ *             2^31 - 2^18); seq_len above table_width * page is taken as that.
  *   nseq      sequences (0 is valid: nothing is done).
  * The arrays are read on the device only.  Whatever they hold, every access
  * stays in bounds: offsets and lengths are clamped, a position whose page id
@@ -473,9 +473,10 @@ typedef struct {
  *   interleaved  1: pair j is channels 2j and 2j + 1; 0: j and j + rot / 2.
  *   q, q_heads, q_out  bf16 [N, q_heads, d]: the new tokens' queries, turned
  *             the same way into q_out (rounded to nearest even; may be q
- *             itself, may not overlap it otherwise: IDX_EINVAL); q_heads = 0:
- *             none.  The rows of q_out must not overlap: one of its strides spans the
- *             whole of the other (IDX_EINVAL).
+ *             itself, may not overlap it otherwise: IDX_EINVAL; nor k or v, which is
+ *             not checked); q_heads = 0: none.  The rows of q_out must not
+ *             overlap: one of its strides spans the whole of the other
+ *             (IDX_EINVAL).
  * Positions at or past table_width * page or (with a rotation) rope_rows are
  * not written, nor are their queries when past rope_rows.
  * IDX_BF16 rounds to nearest even.  IDX_FP8_E4M3: a page's scale for a head
@@ -484,7 +485,8 @@ typedef struct {
  * or stays what it is when that is larger and the page holds tokens of the
  * sequence already (seq_len[i] not a multiple of page).  When it grows, the
  * held tokens' codes are brought to the new scale, rounded to nearest even;
- * codes are x / s rounded likewise.  An infinite or NaN element is stored as
+ * codes are x * (1 / s) rounded likewise (exact products where s is a power of
+ * two, as every scale is that a call has set).  An infinite or NaN element is stored as
  * NaN.  Slots behind the appended tokens keep what they hold.
  * A page must not be written for two sequences in one call.
  */
@@ -508,9 +510,9 @@ int indexer_kv_append(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs
  *             page); sizes the split along the keys and the workspace.  A
  *             longer sequence breaks the precondition: its rows' results are
  *             unspecified, every access stays in bounds.
- *   out       device bf16 [S, q_heads, d], contiguous, 16-byte aligned; may not
- *             overlap q (IDX_EINVAL).
- *   lse       device fp32 [S, q_heads] or NULL.
+ *   out       device bf16 [S, q_heads, d], contiguous, 16-byte aligned.
+ *   lse       device fp32 [S, q_heads] or NULL.  Neither output may overlap q
+ *             or the other (IDX_EINVAL).
  *   workspace device, 16-byte aligned, of at least
  *             indexer_kv_attend_workspace_bytes(...) bytes for the same sizes
  *             (NULL when that is 0).  Calls that share one must be ordered.
@@ -520,7 +522,8 @@ int indexer_kv_append(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs
  * q and the tokens within seq_len finite, scales positive; everything else in
  * the cache (unused pages, slots past seq_len, their scales) may hold
  * anything, NaN included.  Results do not depend on timing: the same call
- * gives the same bits.
+ * gives the same bits.  The kernel is chosen by the average rows of a sequence:
+ * prompts and single tokens are served faster by a call each than by one.
  */
 int indexer_kv_attend(const indexer_kv_cache *cache, const indexer_kv_seqs *seqs,
                       const indexer_kv_rows *q, int64_t S, int q_heads, float scale, int causal,
@@ -539,7 +542,7 @@ int indexer_kv_attend_workspace_bytes(const indexer_kv_cache *cache, const index
  * entries outside [0, seq_len[i]), -1 among them, are ignored.  In the
  * sequence's cache a position is whatever the indexer's entries count: tokens
  * (m = 1, or IDX_EXPAND), or compressed blocks.
- *   idx       device int32 [S, W], contiguous; any order, a position given
+ *   idx       device int32 [S, W], contiguous (W < 2^31 - 2^18); any order, a position given
  *             twice counts twice.
  *   valid_len device int32 [S].
  *   idx0      device int32 [nseq] or NULL (0): the entry of each sequence's

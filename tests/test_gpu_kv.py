@@ -315,6 +315,71 @@ def test_a_table_of_no_width_holds_nothing():
         assert torch.equal(before, cache.k.view(torch.uint8))
 
 
+def test_a_batch_without_rows():
+    cache = dsai.KVCache.allocate(4, 2, 64, page=16, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    q = torch.empty((0, 4, 64), dtype=BF16, device=DEV)
+    idx = torch.empty((0, 9), dtype=torch.int32, device=DEV)
+    for args in ((i32(0), i32(), torch.empty((0, 3), dtype=torch.int32, device=DEV)),
+                 (i32(0, 0), i32(5), i32(0, 1, 2)[None])):
+        assert cache.attend(q, *args).shape == q.shape
+        assert cache.attend_selected(q, idx, i32(), *args).shape == q.shape
+        assert cache.append(q[:, :2], q[:, :2], *args, q=q).shape == q.shape
+
+
+@pytest.mark.parametrize("c", [ATTEND[6], ATTEND[18], ATTEND[19]], ids=["rows", "tiles", "ragged"])
+def test_factors_that_underflow_leave_masked_positions_masked(c):
+    """Key scales of 2^-117 and a factor of 1e-38: every score is 0 in fp32, the
+    mask still counts, and what a row sees weighs the same."""
+    dtype, d, page, heads, group, lens, rows, causal, pad = c
+    pr = Problem(13, FP8, heads, d, page, lens)
+    pr.scale["k"] = np.where(np.isfinite(pr.scale["k"]), np.float32(2.0 ** -117), np.float32(np.nan))
+    cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    q = pr.queries(sum(rows), heads * group)
+    ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
+                     pr.cache["v"], pr.scale["v"], 1e-38)
+    out, lse = pr.gpu().attend(q.to(DEV), dev(cu), dev(pr.lens), dev(pr.table), scale=1e-38,
+                               with_lse=True)
+    check(out, lse, ref, d, "underflow")
+
+
+@pytest.mark.parametrize("rows,group", [(1, 1), (1, 128)], ids=["rows", "tiles"])
+def test_a_sequence_of_nearly_2_31_positions(rows, group):
+    """All pages but the last are page 0 (score 0, value 1), the last is page 1
+    (score 16, value -1): o = (n - 128 - 128 e^16) / (n - 128 + 128 e^16).
+
+    The sums of ones are exact (below 2^24 a lane).  e^16 comes from an exponent
+    of 24 bits below 32, off by 2^-20, so by 2^-20 relative, and exp2's last
+    step; the parts, at most 512, are added in fp32: 2^-15.  Together below 2^-14."""
+    page, width = 128, 2 ** 31 // 128 - 2 ** 18 // 128 - 1
+    n = page * width
+    k = torch.zeros((2, 1, page, 64), device=DEV)
+    k[1, :, :, 0] = 16
+    v = torch.ones((2, 1, page, 64), device=DEV)
+    v[1] = -1
+    one = torch.ones((2, 1), device=DEV)
+    cache = dsai.KVCache(k.to(FP8), v.to(FP8), k_scale=one, v_scale=one)
+    table = torch.zeros((1, width), dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    q = torch.zeros((rows, group, 64), dtype=BF16, device=DEV)
+    q[:, :, 0] = 1
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    out, lse = cache.attend(q, i32(0, rows), i32(n), table, scale=1.0, with_lse=True)
+    big, rest = 128 * np.exp(16.0), float(n - 128)
+    o, l = (rest - big) / (rest + big), np.log(rest + big)
+    assert float((out.double() - o).abs().max()) <= 2.0 ** -8 * o + 2.0 ** -13
+    assert float((lse.double() - l).abs().max()) <= 2.0 ** -14 + 2.0 ** -21 * (1 + l)
+    # selected positions at both ends, by one row and by pairs of rows
+    for S in (1, 1024):
+        idx = i32(0, 5, n - 129, n - 128, n - 1, n, -1).repeat(S, 1)
+        qs = q[:1, :1].expand(S, 1, 64)
+        out, lse = cache.attend_selected(qs, idx, i32(7).repeat(S), i32(0, S), i32(n), table,
+                                         scale=1.0, with_lse=True)
+        o, l = (3 - 2 * np.exp(16.0)) / (3 + 2 * np.exp(16.0)), np.log(3 + 2 * np.exp(16.0))
+        assert float((out.double() - o).abs().max()) <= 2.0 ** -8 + 2.0 ** -13
+        assert float((lse.double() - l).abs().max()) <= 2.0 ** -14 + 2.0 ** -21 * (1 + l)
+
+
 @pytest.mark.parametrize("group", [4, 64])
 @pytest.mark.parametrize("dtype", [FP8, BF16])
 def test_pages_that_do_not_exist_are_masked(dtype, group):
@@ -670,6 +735,56 @@ def test_a_decode_step_replays_from_a_graph():
             t.copy_(torch.randn(t.shape, generator=g, device=DEV).to(BF16) * (r + 1))
         held += 1
         after += 1
+
+
+def test_a_prompt_replays_from_a_graph():
+    """append of a chunk, attention of its rows in parts along the keys and over
+    pairs of selections, captured once and replayed on new tokens with other work
+    between; two graphs with workspaces of their own."""
+    H, G, d, page, held, n, W = 2, 8, 64, 16, 900, 600, 64
+    width = -(-(held + n) // page)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    table = torch.randperm(width, generator=g, device=DEV).int()[None]
+    cu, before, after = i32(0, n), i32(held), i32(held + n)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV).to(BF16)  # noqa: E731
+    cache, twin = (dsai.KVCache.allocate(width, H, d, page=page, device=DEV) for _ in range(2))
+    old = rand(held, H, d)
+    for c in (cache, twin):
+        c.append(old, old, i32(0, held), i32(0), table)
+    k, v, q = rand(n, H, d), rand(n, H, d), rand(n, H * G, d)
+    idx = torch.randint(0, held, (n, W), generator=g, device=DEV).sort(1).values.int()
+    vl = torch.randint(0, W + 1, (n,), generator=g, device=DEV).int()
+
+    def space():
+        sizes = (cache.attend_workspace_bytes(n, H * G, 1, width),
+                 cache.attend_selected_workspace_bytes(n, H * G, 1, W))
+        assert min(sizes) > 0
+        return [torch.full((s,), 0xff, dtype=torch.uint8, device=DEV) for s in sizes], \
+            [(torch.empty_like(q), torch.empty((n, H * G), device=DEV)) for _ in range(2)]
+
+    def step(c, ws, outs):
+        c.append(k, v, cu, before, table)
+        c.attend(q, cu, after, table, with_lse=True, workspace=ws[0], out=outs[0])
+        c.attend_selected(q, idx, vl, cu, after, table, with_lse=True, workspace=ws[1], out=outs[1])
+
+    mine = [space(), space()]
+    step(cache, *mine[0])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in mine]
+    for graph, (ws, outs) in zip(graphs, mine):
+        with torch.cuda.graph(graph):
+            step(cache, ws, outs)
+    for r in range(4):
+        graphs[r % 2].replay()
+        ws, outs = space()
+        step(twin, ws, outs)
+        torch.cuda.synchronize()
+        for (a, b), (x, y) in zip(mine[r % 2][1], outs):
+            assert torch.equal(a, x) and torch.equal(b, y), r
+        for t in (k, v, q):
+            t.copy_(rand(*t.shape))
+        idx.copy_(torch.randint(0, held, (n, W), generator=g, device=DEV).sort(1).values.int())
 
 
 def test_calls_run_on_the_current_stream():

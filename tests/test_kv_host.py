@@ -13,6 +13,7 @@ from oracle import kv as okv
 
 P = 1 << 20          # pointers that are never followed: 16-byte aligned
 OUT = P + (1 << 40)
+LSE = P + (1 << 41)
 
 
 def cache(**kw):
@@ -53,14 +54,14 @@ BAD_SEQS = [
 ]
 
 
-def attend(c=None, s=None, q=None, S=5, q_heads=8, scale=0.1, causal=1, max_len=0, out=OUT, lse=P,
-           ws=None, n=0):
+def attend(c=None, s=None, q=None, S=5, q_heads=8, scale=0.1, causal=1, max_len=0, out=OUT,
+           lse=LSE, ws=None, n=0):
     return _lib.load().indexer_kv_attend(c or cache(), s or seqs(), q or rows(), S, q_heads, scale,
                                          causal, max_len, out, lse, ws, n, None)
 
 
 def selected(c=None, s=None, q=None, S=5, q_heads=8, scale=0.1, idx=P, W=9, vl=P, idx0=None,
-             out=OUT, lse=P, ws=None, n=0):
+             out=OUT, lse=LSE, ws=None, n=0):
     return _lib.load().indexer_kv_attend_selected(c or cache(), s or seqs(), q or rows(), S,
                                                   q_heads, scale, idx, W, vl, idx0, out, lse, ws,
                                                   n, None)
@@ -90,6 +91,9 @@ def test_bad_arguments_of_attend_are_refused():
             assert fn(**kw) == _lib.IDX_EINVAL, kw
         assert fn(S=2 ** 29) == _lib.IDX_EUNSUPPORTED
         assert fn(S=0) == 0 and fn(s=seqs(nseq=0)) == 0       # nothing to do
+    empty = dict(idx=None, vl=None, q=rows(None), out=None, lse=None)
+    assert selected(S=0, **empty) == 0 and selected(s=seqs(nseq=0), **empty) == 0
+    assert attend(S=0, q=rows(None), out=None, lse=None) == 0
     for kw in (dict(causal=2), dict(max_len=-1)):
         assert attend(**kw) == _lib.IDX_EINVAL
     for kw in (dict(W=0), dict(idx=None), dict(vl=None), dict(idx=P + 2), dict(idx0=P + 1)):
@@ -102,6 +106,9 @@ def test_outputs_that_overlap_the_queries_are_refused():
     for fn in (attend, selected):
         for out in (P, P + 16, far - 16, P - 2 * 5 * 8 * 128 + 16):
             assert fn(out=out) == _lib.IDX_EINVAL, out
+            assert fn(lse=out if out >= P else P - 4) == _lib.IDX_EINVAL, out
+        for lse in (OUT, OUT + 2 * 5 * 8 * 128 - 4, OUT - 4):
+            assert fn(lse=lse) == _lib.IDX_EINVAL, lse
     ok = dict(q=rows(), q_heads=2)
     for q_out in (rows(P + 16), rows(P, 512, 128), rows(P, 256, 1280), rows(P + 2 * 4 * 256)):
         assert append(q_out=q_out, **ok) == _lib.IDX_EINVAL
@@ -156,6 +163,23 @@ def test_workspace_is_asked_for_exactly_when_rows_are_split():
     assert selected(s=wide, S=1, q_heads=16, W=2048) == _lib.IDX_EWORKSPACE
     assert sel(1, 0)[0] == _lib.IDX_EINVAL
     assert lib.indexer_kv_attend_workspace_bytes(cache(), wide, 1, 16, 0, None) == _lib.IDX_EINVAL
+
+
+def test_positions_are_counted_in_32_bits_with_room_to_spare():
+    """2^31 - 2^18 positions of a sequence, or entries of a row, are too many."""
+    lib, n = _lib.load(), ctypes.c_size_t()
+    for page in (16, 128):
+        for width, code in ((2 ** 31 // page - 2 ** 18 // page, _lib.IDX_EUNSUPPORTED),
+                            (2 ** 31 // page - 2 ** 18 // page - 1, 0)):
+            s = seqs(table_width=width, table_stride=width)
+            assert lib.indexer_kv_attend_workspace_bytes(cache(page=page), s, 1, 8, 0,
+                                                         ctypes.byref(n)) == code
+            if code:
+                for call in (attend, selected, append):
+                    assert call(c=cache(page=page), s=s) == code
+    assert selected(W=2 ** 31 - 2 ** 18) == _lib.IDX_EUNSUPPORTED
+    assert lib.indexer_kv_attend_selected_workspace_bytes(
+        cache(), seqs(), 1, 8, 2 ** 31 - 2 ** 18, ctypes.byref(n)) == _lib.IDX_EUNSUPPORTED
 
 
 def test_the_binding_refuses_tensors_that_are_not_a_cache():
