@@ -193,6 +193,26 @@ void rows_kernel(KvAttendParams p)
     const int head = blk.head, grp = blk.grp, split = blk.split;
     const int64_t slot = p.slot0 + blk.slot;
 
+    // The selection comes while the sequence is looked up: entries of the list
+    // before it is known how many count (they lie in the row all the same).
+    const int e0 = split * p.chunk;
+    uint32_t raw[kList / 256];           // selected positions, or picked cache slots
+    const int64_t entry0 = SEL ? slot * p.W : PAIR ? blk.slot * 2 * p.W : 0;
+    const int held = SEL ? p.W : 2 * p.W;
+    const uint32_t *given = SEL ? reinterpret_cast<const uint32_t *>(p.idx) : p.pick;
+    auto fetch = [&](int s0, int end) KV_INLINE {
+#pragma unroll
+        for (int k = 0; k < kList / 256; ++k) {
+            const int i = s0 + tid + 256 * k;
+            raw[k] = i < end ? given[entry0 + i] : 0;
+        }
+    };
+    int count = 0;
+    int4 picked = {};            // positions of both rows, of the first, of the second
+    if constexpr (SEL) count = p.valid_len[slot];
+    if constexpr (PAIR) picked = p.pick_n[blk.slot];
+    if constexpr (!ALL) fetch(e0, held);
+
     const int R = SEL ? 1 : p.tile_rows;
     const Seq sq = find_seq(kc, p.S, slot, R, SEL ? 0 : 1);
     const int seq = sq.i, c0 = sq.c0;
@@ -204,18 +224,15 @@ void rows_kernel(KvAttendParams p)
     const int64_t row0 = c0 + t0;
     // entries: keys 0 .. entries of the sequence, or of the row's selection
     int entries, base = 0;
-    int4 picked = {};            // positions of both rows, of the first, of the second
     if constexpr (SEL) {
-        entries = clamped(p.valid_len[row0], p.W);
+        entries = clamped(count, p.W);
         base = p.idx0 ? p.idx0[seq] : 0;
     } else if constexpr (PAIR) {
-        picked = p.pick_n[blk.slot];
         entries = picked.x + picked.y + picked.z;
     } else {
         const int64_t last = p.causal ? (int64_t)len - rows_in_seq + t0 + ntok : len;
         entries = clamped(last < 0 ? 0 : (int)last, len);
     }
-    const int e0 = split * p.chunk;
     if (split > 0 && e0 >= entries) return;
     const int e1 = entries - e0 < p.chunk ? entries : e0 + p.chunk;
 
@@ -362,11 +379,10 @@ void rows_kernel(KvAttendParams p)
             there[k] = i < cnt;
             pos[k] = s0 + i;
             if constexpr (SEL) {
-                pos[k] = (int64_t)(there[k] ? p.idx[row0 * p.W + pos[k]] : -1) - base;
+                pos[k] = (int64_t)(int)raw[k] - base;
                 there[k] = there[k] && pos[k] >= 0 && pos[k] < len;
             }
-            if constexpr (PAIR)
-                pos[k] = there[k] ? p.pick[blk.slot * 2 * p.W + pos[k]] : 0;
+            if constexpr (PAIR) pos[k] = raw[k];
         }
 #pragma unroll
         for (int k = 0; k < kList / 256; ++k) {
@@ -375,6 +391,7 @@ void rows_kernel(KvAttendParams p)
             else
                 id[k] = there[k] ? (uint32_t)table[pos[k] >> kc.page_shift] : kNoPage;
         }
+        float ks[FP8 ? kList / 256 : 1], vs[FP8 ? kList / 256 : 1];
 #pragma unroll
         for (int k = 0; k < kList / 256; ++k) {
             const int i = tid + 256 * k;
@@ -382,12 +399,10 @@ void rows_kernel(KvAttendParams p)
             const uint32_t unit = there[k] ? id[k] * (uint32_t)kc.heads + head : 0;
             const uint64_t row = ((uint64_t)unit << kc.page_shift) +
                                  (there[k] ? (int)pos[k] & page_mask : 0);
-            if (i < padded) {
-                sm.list.off[i] = row * (uint64_t)(D * TL::ES);
-                if constexpr (FP8) {
-                    sm.list.ks[i] = there[k] ? kc.k_scale[unit] * p.c2 : 0.0f;
-                    sm.list.vs[i] = there[k] ? kc.v_scale[unit] : 0.0f;
-                }
+            if (i < padded) sm.list.off[i] = row * (uint64_t)(D * TL::ES);
+            if constexpr (FP8) {
+                ks[k] = there[k] ? kc.k_scale[unit] : 0.0f;
+                vs[k] = there[k] ? kc.v_scale[unit] : 0.0f;
             }
             const uint64_t bad = __ballot(!there[k]);
             if (lane == 0) {
@@ -398,9 +413,23 @@ void rows_kernel(KvAttendParams p)
         __syncthreads();
 
         // ---- tiles of 32 keys, in turn over the waves, the next one's loads ahead
+        // (the first one's along with the scales and the next list's entries)
         ST next;
         int at = wave * 32;
         if (at < padded) next.load(kb, vb, sm.list.off + at, lane);
+        if constexpr (!ALL)
+            if (s0 + kList < e1) fetch(s0 + kList, e1);
+        if constexpr (FP8) {
+#pragma unroll
+            for (int k = 0; k < kList / 256; ++k) {
+                const int i = tid + 256 * k;
+                if (i < padded) {
+                    sm.list.ks[i] = ks[k] * p.c2;
+                    sm.list.vs[i] = vs[k];
+                }
+            }
+            __syncthreads();
+        }
         for (; at < padded; at += 128) {
             next.put(stage, (uint32_t)uniform((int)sm.list.bad[at >> 5]), lane);
             if (at + 128 < padded) next.load(kb, vb, sm.list.off + at + 128, lane);
