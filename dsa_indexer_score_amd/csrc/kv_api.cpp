@@ -124,17 +124,23 @@ struct Plan {
     int64_t slots, part_ml, bytes;
 };
 
-// Two blocks for each CU: 262,144 keys, 8 key heads, one row take 105 us with
-// 512 blocks, 111 with 768.  A part below 512 keys costs more in the join than
-// it saves (4 rows of 517 keys: 11.3 against 15.7 us a call with parts of 256;
-// 16 rows of 2,048 selected keys, whose looking up takes longer: 16.8 us with
-// parts of 256, 17.2 with 512).  64
-// rows of up to 16,384 keys: 258 us with parts of 4,096, 272 with 8,192, 264
-// with 2,048.
+constexpr int64_t kCus = 256;
+// Parts of a row's keys in the row kernel (microseconds of GPU time, e4m3, d =
+// 128, 8 key heads).  Two blocks for each CU where single rows are few or parts
+// are long, one otherwise: 4 rows of 4,096 keys 13.5 with 512 blocks, 15.0 with
+// 256, but 16 rows of 4,096 keys 35.7 with 512, 32.3 with 256; 262,144 keys, one
+// row, 105 with 512, 111 with 768.  Selected keys: one (4 rows of 4,096: 13.8
+// with 256, 15.1 with 512).  A join costs what some 768 keys do: 16 rows of 1,024
+// keys 12.6 in one part, 14.8 in two; one row of 1,024 11.5 in one part, 9.6 in
+// eight.  A part of 128 keys is one round of a block's waves (one row of 2,048
+// keys: 9.3 with 16 parts, 10.5 with 8); selected keys, which take longer to look
+// up, go by 256 (11.0 with 16, 10.5 with 8).  64 rows of up to 16,384 keys: 258
+// with parts of 4,096, 272 with 8,192, 264 with 2,048.
 constexpr int64_t kFillBlocks = 512;
 constexpr int64_t kFillWaves = 4096;
-constexpr int64_t kMinChunk = 512, kMinPicked = 256;
-constexpr int64_t kRaggedChunk = 4096;
+constexpr int64_t kMinChunk = 128, kMinPicked = 256;
+constexpr int64_t kLongChunk = 4096, kFewUnits = 64;
+constexpr int64_t kJoinKeys = 768;
 // Columns (query rows of a sequence x query heads of a key head) up to which a
 // sequence's rows go by blocks of 32 columns, straight from memory.
 constexpr int64_t kFewCols = 64;
@@ -142,7 +148,6 @@ constexpr int kTilesHeads = 64;       // query heads of a key head in a block of
 // Lists of one launch's pairs: 256 MB, about 16,000 pairs of 2,048 positions;
 // more rows take several launches.
 constexpr int64_t kPickBytes = int64_t(1) << 28;
-constexpr int64_t kCus = 256;
 constexpr int64_t kMinTileChunk = 512;
 
 Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int64_t max_len,
@@ -162,7 +167,8 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
         p.tile_rows = selected ? 1 : 16 * p.nt / p.head_tile;
     }
     p.slots = selected ? S : S / p.tile_rows + nseq;
-    const int64_t units = std::max<int64_t>(1, S / p.tile_rows) * c->heads * p.groups;
+    // row tiles with rows: a sequence's last one is not full
+    const int64_t units = std::max(S / p.tile_rows, std::min<int64_t>(S, nseq)) * c->heads * p.groups;
     // Pairs of rows share what they both select: where 16 columns hold a row's
     // heads and the pairs alone fill the GPU.
     if (selected && group <= 16 && max_len <= dsai::kKvPairWidth && S >= 2 * (int64_t)nseq &&
@@ -193,11 +199,14 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
             units * seen / kCus * (c->d == 64 ? 3 : 5) / 4, 1);
         nsplit = std::min(div_up(keys, share), keys / kMinTileChunk);
     } else {
-        // parts that fill the GPU, as far as they are worth a block each; among
-        // several sequences parts of at most kRaggedChunk keys, so that the
+        // parts that fill the GPU, where they save more than the join takes; among
+        // several sequences parts of at most kLongChunk keys, so that the
         // longest does not trail the others
-        nsplit = std::min(kFillBlocks / units, keys / (selected ? kMinPicked : kMinChunk));
-        if (!selected && nseq > 1) nsplit = std::max(nsplit, keys / kRaggedChunk);
+        const int64_t fill = !selected && units <= kFewUnits ? kFillBlocks : kCus;
+        nsplit = std::max(std::min(fill / units, keys / (selected ? kMinPicked : kMinChunk)),
+                          std::min(kFillBlocks / units, keys / kLongChunk));
+        if (nsplit > 1 && keys - keys / nsplit < kJoinKeys) nsplit = 1;
+        if (!selected && nseq > 1) nsplit = std::max(nsplit, keys / kLongChunk);
     }
     nsplit = std::max<int64_t>(nsplit, 1);
     int64_t chunk = round_up(div_up(keys, nsplit), 128);
