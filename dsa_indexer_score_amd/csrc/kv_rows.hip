@@ -27,7 +27,15 @@
 // probabilities.
 //
 // Blocks that share a row (more keys than one chunk) write (o, m, l) to the
-// workspace and kv_join adds them up; the order is fixed, so results repeat.
+// workspace and join_kernel adds them up; the order is fixed, so results repeat.
+//
+// Bound by memory where keys are many: 262,144 keys of 8 heads (e4m3, d = 128)
+// for one row of 64 heads take 98 us with the join, 5.5 TB/s (a large copy: 4.7);
+// 64 rows of up to 16,384 keys 238 us, 4.7 TB/s.  With few keys it is the chain of
+// dependent loads (sequence, page, row): 5.5 us for 128 keys, 0.9 us for each 128
+// more in a block.  2,048 rows with 2,048 selected positions each (64 / 8 heads)
+// take 497 us, bound by the vector unit, which widens 256 codes a key and query
+// row pair for 16 columns.
 #include "kv_common.h"
 
 namespace dsai {

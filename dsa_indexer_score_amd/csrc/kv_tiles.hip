@@ -24,6 +24,11 @@
 // when a score exceeds it by more than 2^8, so that O is rarely rescaled; the
 // probabilities are at most 2^8 then, in fp32 sums and bf16 operands that lose
 // nothing by it.
+//
+// Bound by the matrix unit and the exponentials beside it, which overlap little:
+// 4,096 rows behind 28,672 keys (e4m3, d = 128, 32 / 8 heads) take 1.95 to 2.05
+// ms, 1.0 PFLOP/s (a large matrix product: 1.4); at d = 64, with twice the
+// exponentials for each product, 0.55 PFLOP/s.
 #include <type_traits>
 
 #include "kv_common.h"
