@@ -283,11 +283,13 @@ void rows_kernel(KvAttendParams p)
     }
     minlim = uniform(minlim);
 
+    // The running maximum is ref, once thr is not -inf; before, nothing was seen.
     kvf4 o[NT][MT];
-    float mx[NT], l[NT];
+    float ref[NT], thr[NT], l[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        mx[t] = -__builtin_inff();
+        ref[t] = 0.0f;
+        thr[t] = -__builtin_inff();
         l[t] = 0.0f;
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[t][i] = kvf4{0, 0, 0, 0};
@@ -332,8 +334,15 @@ void rows_kernel(KvAttendParams p)
         for (int t = 0; t < NT; ++t) {
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = acc[t][j >> 2][j & 3] * (FP8 ? ks[j] : p.c2);
-            if (bad || edge) {
+            for (int j = 0; j < 8; ++j)
+                x[j] = __builtin_fmaf(acc[t][j >> 2][j & 3], FP8 ? ks[j] : p.c2, -ref[t]);
+            // a pair's tile mostly lies in one list: a column sees all of it or nothing
+            const int e = s0 + at;
+            const bool all = PAIR && e >= lim[t] && e + 32 <= end[t];
+            if (PAIR && edge && !bad && !__ballot(!all && e + 32 > lim[t] && e < end[t])) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = all ? -__builtin_inff() : x[j];
+            } else if (bad || edge) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int key = 16 * (j >> 2) + 4 * g + (j & 3);
@@ -345,18 +354,21 @@ void rows_kernel(KvAttendParams p)
             float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
                               fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
             top = max_over_rows(top);
-            if (__ballot(top > mx[t] + kSlack)) {  // also the first tile: mx = -inf
-                const float m2 = fmaxf(mx[t], top);
-                const float a = mx[t] == m2 ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - m2);
-                mx[t] = m2;
+            if (__ballot(top > thr[t])) {          // also the first tile
+                const bool some = top > -__builtin_inff();
+                const float up = thr[t] > 0.0f ? fmaxf(top, 0.0f) : some ? top : 0.0f;
+                const float a = __builtin_amdgcn_exp2f(thr[t] > 0.0f ? -up : 0.0f);
+                ref[t] += up;
+                thr[t] = some ? kSlack : thr[t];
                 l[t] *= a;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[t][i] *= a;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] -= up;
             }
-            const float m1 = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[j] = __builtin_amdgcn_exp2f(x[j] - m1);
+                x[j] = __builtin_amdgcn_exp2f(x[j]);
                 l[t] += x[j];
                 if constexpr (FP8) x[j] *= vs[j];
             }
@@ -446,9 +458,10 @@ void rows_kernel(KvAttendParams p)
     }
 
     // ---- join the waves
-    float f[NT];
+    float f[NT], mx[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+        mx[t] = thr[t] > 0.0f ? ref[t] : -__builtin_inff();
         l[t] += __shfl_xor(l[t], 16);
         l[t] += __shfl_xor(l[t], 32);
         if (g == 0) {
