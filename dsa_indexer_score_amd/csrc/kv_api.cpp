@@ -261,7 +261,9 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
         return IDX_EINVAL;
     const Plan pl = make_plan(c, S, q_heads, s->nseq, idx ? W : most_keys(c, s, max_len),
                               idx != nullptr);
-    if ((pl.slots * pl.nsplit * c->heads + 8) * pl.groups >= INT32_MAX) return IDX_EUNSUPPORTED;
+    // (in double: the product of the largest sizes passes 64 bits)
+    if (((double)pl.slots * pl.nsplit * c->heads + 8) * pl.groups >= INT32_MAX)
+        return IDX_EUNSUPPORTED;
     if (pl.bytes > 0 && (!workspace || workspace_bytes < (size_t)pl.bytes || !aligned(workspace, 16)))
         return IDX_EWORKSPACE;
 
