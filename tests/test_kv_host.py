@@ -178,14 +178,12 @@ def test_positions_are_counted_in_32_bits_with_room_to_spare():
                 for call in (attend, selected, append):
                     assert call(c=cache(page=page), s=s) == code
     assert selected(W=2 ** 31 - 2 ** 18) == _lib.IDX_EUNSUPPORTED
-    # blocks of a launch: the product of sequences, parts and heads passes 2^64;
-    # a selection's go by rows, and those of one row fit
+    # blocks of a launch: the product of sequences, parts and heads passes 2^64
     many = dict(c=cache(pages=1, heads=65535, page=16), S=1, q_heads=65535, q=rows(P, 0, 128),
                 lse=LSE)
     wide = 2 ** 27 - 2 ** 14 - 1
     s = seqs(nseq=2 ** 30 - 2, table_width=wide, table_stride=wide)
     assert attend(s=s, **many) == _lib.IDX_EUNSUPPORTED
-    assert selected(s=s, W=2 ** 20, **many) == _lib.IDX_EWORKSPACE
     assert lib.indexer_kv_attend_selected_workspace_bytes(
         cache(), seqs(), 1, 8, 2 ** 31 - 2 ** 18, ctypes.byref(n)) == _lib.IDX_EUNSUPPORTED
 
