@@ -52,10 +52,11 @@ struct KvAttendParams {
     int W;
     const int32_t *valid_len;
     const int32_t *idx0;      // [nseq] or null, subtracted from the entries
-    // selected positions of pairs of rows, as launch_kv_pick writes them (or
-    // null): per slot 2 W entries and their counts
-    uint32_t *pick;
-    int4 *pick_n;
+    // selected positions of tile_rows neighbouring rows, as launch_kv_pick writes
+    // them (or null): per slot tile_rows * W entries, for each row of the slot a bit
+    // for each entry (which it has), and the number of entries
+    uint32_t *pick, *pick_rows;
+    int *pick_n;
     // the split: `chunk` keys a block, nsplit blocks along the keys; rows that
     // need more than one leave (o, m, l) in part_o / part_ml for the join
     int head_tile, groups;    // query heads of a key head that a block takes, blocks for all
@@ -79,11 +80,12 @@ inline int64_t kv_blocks(const KvAttendParams &p)
 hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hipStream_t st);
 // 256 columns per block: many query rows
 hipError_t launch_kv_tiles(int dtype, int d, const KvAttendParams &p, hipStream_t st);
-// The lists of p.slots pairs of rows into p.pick (W at most kKvPairWidth)
+// The lists of p.slots times tile_rows (2 or 4) rows (W at most kKvSharedWidth)
 hipError_t launch_kv_pick(const KvAttendParams &p, hipStream_t st);
 hipError_t launch_kv_join(int d, const KvAttendParams &p, hipStream_t st);
 
-constexpr int kKvPairWidth = 4096; // entries of a row that launch_kv_pick takes
+constexpr int kKvSharedWidth = 4096; // entries of a row that launch_kv_pick takes
+constexpr int kKvSharedRows = 4;     // rows that share a list at most
 constexpr int kKvRowsCols = 32;   // columns of a launch_kv_rows block at most
 constexpr int kKvTileCols = 256;  // columns of a launch_kv_tiles block
 

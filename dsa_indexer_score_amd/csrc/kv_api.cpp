@@ -118,10 +118,10 @@ dsai::KvCache kernel_cache(const indexer_kv_cache *c, const indexer_kv_seqs *s)
 // How a call is cut into blocks; depends on host sizes only, so that the
 // workspace functions and the calls agree.
 struct Plan {
-    bool tiles, pairs;
+    bool tiles, shared;
     int64_t pass;             // slots of a launch
     int nt, head_tile, groups, tile_rows, nsplit, chunk;
-    int64_t slots, part_ml, bytes;
+    int64_t slots, part_ml, pick_n, pick_rows, bytes;
 };
 
 constexpr int64_t kCus = 256;
@@ -145,9 +145,15 @@ constexpr int64_t kJoinKeys = 768;
 // sequence's rows go by blocks of 32 columns, straight from memory.
 constexpr int64_t kFewCols = 64;
 constexpr int kTilesHeads = 64;       // query heads of a key head in a block of 256 columns
-// Lists of one launch's pairs: 256 MB, about 16,000 pairs of 2,048 positions;
-// more rows take several launches.
+// Lists of one launch's groups of rows: 256 MB, about 26,000 rows of 2,048
+// positions; more rows take several launches.
 constexpr int64_t kPickBytes = int64_t(1) << 28;
+// Four rows share their selections rather than two where that fills 16 columns
+// that two leave empty (2,048 rows x 2,048 of 65,536, 32 / 8 heads, e4m3: 322 us
+// against 455), or, with 5 to 8 heads a key head, takes 32 columns in place of 16
+// and leaves several rounds of blocks (64 / 8 heads: 455 against 473, bf16 542
+// against 624; 777 rows of 4 key heads, one round: 96 against 90).
+constexpr int64_t kManyBlocks = 2048;
 constexpr int64_t kMinTileChunk = 512;
 
 Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int64_t max_len,
@@ -169,20 +175,22 @@ Plan make_plan(const indexer_kv_cache *c, int64_t S, int q_heads, int nseq, int6
     p.slots = selected ? S : S / p.tile_rows + nseq;
     // row tiles with rows: a sequence's last one is not full
     const int64_t units = std::max(S / p.tile_rows, std::min<int64_t>(S, nseq)) * c->heads * p.groups;
-    // Pairs of rows share what they both select: where 16 columns hold a row's
-    // heads and the pairs alone fill the GPU.
-    if (selected && group <= 16 && max_len <= dsai::kKvPairWidth && S >= 2 * (int64_t)nseq &&
+    // Neighbouring rows share what they select: where 16 columns hold a row's
+    // heads and such groups of rows alone fill the GPU.
+    if (selected && group <= 16 && max_len <= dsai::kKvSharedWidth && S >= 2 * (int64_t)nseq &&
         S / 2 * c->heads >= kFillBlocks && c->pages * c->page <= (int64_t)UINT32_MAX) {
-        p.pairs = true;
-        p.tile_rows = 2;
-        p.nt = (int)div_up(2 * group, 16);
-        p.slots = S / 2 + nseq;
-        const int64_t each = 2 * max_len * 4 + 16;
-        p.pass = std::min(p.slots, std::max<int64_t>(kPickBytes / each, 1));
+        p.shared = true;
+        const bool four = group <= 4 || (group <= 8 && S / 4 * c->heads >= kManyBlocks);
+        p.tile_rows = four && S >= 4 * (int64_t)nseq ? 4 : 2;
+        p.nt = (int)div_up(p.tile_rows * group, 16);
+        p.slots = S / p.tile_rows + nseq;
+        const int64_t list = p.tile_rows * max_len, bits = p.tile_rows * div_up(list, 32) * 4;
+        p.pass = std::min(p.slots, std::max<int64_t>(kPickBytes / (list * 4 + bits + 4), 1));
         p.nsplit = 1;
         p.chunk = INT32_MAX;
-        p.part_ml = round_up(p.pass * 2 * max_len * 4, 256);
-        p.bytes = p.part_ml + p.pass * 16;
+        p.pick_n = p.pass * list * 4;
+        p.pick_rows = p.pick_n + p.pass * 4;
+        p.bytes = p.pick_rows + p.pass * bits;
         return p;
     }
     const int64_t keys = std::max<int64_t>(max_len, 1);
@@ -296,14 +304,15 @@ int attend(const indexer_kv_cache *c, const indexer_kv_seqs *s, const indexer_kv
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + pl.part_ml);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (pl.pairs) {
+    if (pl.shared) {
         p.pick = static_cast<uint32_t *>(workspace);
-        p.pick_n = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + pl.part_ml);
+        p.pick_n = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.pick_n);
+        p.pick_rows = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + pl.pick_rows);
     }
     for (p.slot0 = 0; p.slot0 < pl.slots; p.slot0 += pl.pass) {
         p.slots = std::min(pl.pass, pl.slots - p.slot0);
         hipError_t e = hipSuccess;
-        if (pl.pairs) e = dsai::launch_kv_pick(p, st);
+        if (pl.shared) e = dsai::launch_kv_pick(p, st);
         if (e != hipSuccess) return fail_hip(e);
         e = pl.tiles ? dsai::launch_kv_tiles(c->dtype, c->d, p, st)
                      : dsai::launch_kv_rows(c->dtype, c->d, pl.nt, p, st);

@@ -34,8 +34,9 @@
 // 64 rows of up to 16,384 keys 238 us, 4.7 TB/s.  With few keys it is the chain of
 // dependent loads (sequence, page, row): 5.5 us for 128 keys, 0.9 us for each 128
 // more in a block.  2,048 rows with 2,048 selected positions each (64 / 8 heads)
-// take 492 us: the vector unit, which widens 256 codes of a position for 16
-// columns, is busy for 57 % of it, the matrix unit for 16 %, and they overlap little.
+// take 475 us, with 32 / 8 heads 322: the vector unit, which widens 256 codes of a
+// position for 16 columns, is busy for more than half of it, the matrix unit for
+// some 16 %, and they overlap little.
 #include "kv_common.h"
 
 namespace dsai {
@@ -44,7 +45,7 @@ namespace {
 constexpr int kList = 1024;             // keys resolved to rows at a time
 constexpr uint32_t kNoPage = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 of the largest probability against the running maximum
-constexpr int kPickThreads = 512;       // kKvPairWidth / 512 entries of a row each
+constexpr int kPickThreads = 512;       // kKvSharedWidth / 512 entries of a row each
 constexpr int kPickBits = 1 << 17;      // positions that a row's bitmap covers at a time
 constexpr int kFewParts = 16;           // parts that one wave joins
 constexpr float kLn2 = 0.693147180559945309f;
@@ -163,18 +164,18 @@ template <bool FP8, int D> struct Tile {
 };
 
 // What the rows of a block attend to: all of the sequence's tokens, one row's
-// selected positions, or the selections of two neighbouring rows as pick_kernel
-// laid them out (positions of both, of the first, of the second).
-enum { kAll = 0, kSelected = 1, kPairs = 2 };
+// selected positions, or the selections of a few neighbouring rows as pick_kernel
+// put them together (each position once, with the rows that have it).
+enum { kAll = 0, kSelected = 1, kShared = 2 };
 
-// Three blocks a CU where registers allow it and the keys come from the L2 (one
-// or two rows' selections: 752 us with three against 839 with two); streaming
+// Three blocks a CU where registers allow it and the keys come from the L2 (few
+// rows' selections: 752 us with three against 839 with two); streaming
 // all keys from memory two do better (99 against 105 us over 262,144 keys).
 template <bool FP8, int D, int NT, int MODE>
 __global__ __launch_bounds__(256, MODE != kAll && NT == 1 && FP8 ? 3 : 2)
 void rows_kernel(KvAttendParams p)
 {
-    constexpr bool SEL = MODE == kSelected, ALL = MODE == kAll, PAIR = MODE == kPairs;
+    constexpr bool SEL = MODE == kSelected, ALL = MODE == kAll, SHARED = MODE == kShared;
     using TL = Tile<FP8, D>;
     using ST = typename TL::ST;
     constexpr int MT = TL::MT;
@@ -183,6 +184,7 @@ void rows_kernel(KvAttendParams p)
         uint64_t off[kList];            // byte offsets of the keys' rows
         float ks[FP8 ? kList : 4], vs[FP8 ? kList : 4];
         uint32_t bad[kList / 32];       // which of a tile's keys are not there
+        uint32_t has[SHARED ? kKvSharedRows : 1][kList / 32];  // which of them a row has
     };
     struct Join { float o[4][16][PITCH]; };
     struct Work { List list; kvu4 stage[4][64 * ST::NCH]; };
@@ -205,8 +207,10 @@ void rows_kernel(KvAttendParams p)
     // before it is known how many count (they lie in the row all the same).
     const int e0 = split * p.chunk;
     uint32_t raw[kList / 256];           // selected positions, or picked cache slots
-    const int64_t entry0 = SEL ? slot * p.W : PAIR ? blk.slot * 2 * p.W : 0;
-    const int held = SEL ? p.W : 2 * p.W;
+    uint32_t row_has = 0;                // 32 of them, bit by bit, for thread / 32's row
+    const int row_words = (p.tile_rows * p.W + 31) >> 5;
+    const int held = SEL ? p.W : p.tile_rows * p.W;
+    const int64_t entry0 = (SEL ? slot : blk.slot) * held;
     const uint32_t *given = SEL ? reinterpret_cast<const uint32_t *>(p.idx) : p.pick;
     auto fetch = [&](int s0, int end) KV_INLINE {
 #pragma unroll
@@ -214,11 +218,15 @@ void rows_kernel(KvAttendParams p)
             const int i = s0 + tid + 256 * k;
             raw[k] = i < end ? given[entry0 + i] : 0;
         }
+        if constexpr (SHARED) {
+            const int r = tid >> 5, w = (s0 >> 5) + (tid & 31);
+            if (r < p.tile_rows && w < row_words)
+                row_has = p.pick_rows[(blk.slot * p.tile_rows + r) * row_words + w];
+        }
     };
     int count = 0;
-    int4 picked = {};            // positions of both rows, of the first, of the second
     if constexpr (SEL) count = p.valid_len[slot];
-    if constexpr (PAIR) picked = p.pick_n[blk.slot];
+    if constexpr (SHARED) count = p.pick_n[blk.slot];
     if constexpr (!ALL) fetch(e0, held);
 
     const int R = SEL ? 1 : p.tile_rows;
@@ -235,8 +243,8 @@ void rows_kernel(KvAttendParams p)
     if constexpr (SEL) {
         entries = clamped(count, p.W);
         base = p.idx0 ? p.idx0[seq] : 0;
-    } else if constexpr (PAIR) {
-        entries = picked.x + picked.y + picked.z;
+    } else if constexpr (SHARED) {
+        entries = count;
     } else {
         const int64_t last = p.causal ? (int64_t)len - rows_in_seq + t0 + ntok : len;
         entries = clamped(last < 0 ? 0 : (int)last, len);
@@ -246,22 +254,19 @@ void rows_kernel(KvAttendParams p)
 
     // ---- the columns: query rows x heads
     kvb8 q[NT][TL::KS];
-    int lim[NT], end[NT];        // the column sees no entries from lim to end
+    int lim[NT], has[NT];        // the column sees no entries from lim on; its row
     int minlim = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int col = 16 * t + n, tok = col / gsize, hh = grp * gsize + col % gsize;
         const bool in = tok < ntok && hh < p.group;
-        lim[t] = end[t] = 0x7fffffff;
+        lim[t] = 0x7fffffff;
+        has[t] = tok < ntok ? tok : 0;     // of no use where the block has no such row
         if constexpr (ALL) {
             if (in && p.causal) {
                 const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
                 lim[t] = x < 0 ? 0 : (int)x;
             }
-        }
-        if constexpr (PAIR) {
-            lim[t] = tok ? picked.x : picked.x + picked.y;
-            if (tok) end[t] = picked.x + picked.y;
         }
         minlim = lim[t] < minlim ? lim[t] : minlim;
         const uint16_t *src = p.q + (row0 + tok) * p.q_tok +
@@ -305,8 +310,8 @@ void rows_kernel(KvAttendParams p)
     auto process = [&](int s0, int at) KV_INLINE {
         TL cur;
         cur.get_keys(stage, n, g);
-        const uint32_t bad = (uint32_t)uniform((int)sm.list.bad[at >> 5]);
-        const bool edge = !SEL && s0 + at + 32 > minlim;
+        const uint32_t bad = SHARED ? 0 : (uint32_t)uniform((int)sm.list.bad[at >> 5]);
+        const bool edge = ALL && s0 + at + 32 > minlim;
         float ks[8], vs[8];
         auto factors = [&](const float *list, float (&f)[8]) KV_INLINE {
 #pragma unroll
@@ -336,19 +341,21 @@ void rows_kernel(KvAttendParams p)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 x[j] = __builtin_fmaf(acc[t][j >> 2][j & 3], FP8 ? ks[j] : p.c2, -ref[t]);
-            // a pair's tile mostly lies in one list: a column sees all of it or nothing
-            const int e = s0 + at;
-            const bool all = PAIR && e >= lim[t] && e + 32 <= end[t];
-            if (PAIR && edge && !bad && !__ballot(!all && e + 32 > lim[t] && e < end[t])) {
+            if constexpr (SHARED) {
+                const uint32_t own = sm.list.has[has[t]][at >> 5];
+                if (__ballot(own != ~0u)) {
+                    const uint32_t cut = ~own >> (4 * g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = all ? -__builtin_inff() : x[j];
+                    for (int j = 0; j < 8; ++j) {   // all ones where the row has no such key
+                        const uint32_t no = __builtin_amdgcn_sbfe(cut, 16 * (j >> 2) + (j & 3), 1);
+                        x[j] = __uint_as_float((__float_as_uint(x[j]) & ~no) | (0xff800000u & no));
+                    }
+                }
             } else if (bad || edge) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int key = 16 * (j >> 2) + 4 * g + (j & 3);
-                    const bool cut = PAIR ? s0 + at + key >= lim[t] && s0 + at + key < end[t]
-                                          : ALL && s0 + at + key >= lim[t];
-                    if ((bad >> key & 1) || cut) x[j] = -__builtin_inff();
+                    if ((bad >> key & 1) || (ALL && s0 + at + key >= lim[t])) x[j] = -__builtin_inff();
                 }
             }
             float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
@@ -402,11 +409,11 @@ void rows_kernel(KvAttendParams p)
                 pos[k] = (int64_t)(int)raw[k] - base;
                 there[k] = there[k] && pos[k] >= 0 && pos[k] < len;
             }
-            if constexpr (PAIR) pos[k] = raw[k];
+            if constexpr (SHARED) pos[k] = raw[k];
         }
 #pragma unroll
         for (int k = 0; k < kList / 256; ++k) {
-            if constexpr (PAIR)
+            if constexpr (SHARED)
                 id[k] = there[k] ? (uint32_t)(pos[k] >> kc.page_shift) : kNoPage;
             else
                 id[k] = there[k] ? (uint32_t)table[pos[k] >> kc.page_shift] : kNoPage;
@@ -430,6 +437,8 @@ void rows_kernel(KvAttendParams p)
                 sm.list.bad[(i >> 5) + 1] = (uint32_t)(bad >> 32);
             }
         }
+        if constexpr (SHARED)
+            if (tid >> 5 < kKvSharedRows) sm.list.has[tid >> 5][tid & 31] = row_has;
         __syncthreads();
 
         // ---- tiles of 32 keys, in turn over the waves, the next one's loads ahead
@@ -607,42 +616,51 @@ __global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
         p.lse[unit] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_inff();
 }
 
-// The selections of the rows 2 i and 2 i + 1 of a sequence as three lists of
-// cache slots (page id * page size + slot): the positions of both rows, those
-// of the first only, those of the second only, each in the row's order.  Both
-// rows then share what rows_kernel reads of a common position, and all key
-// heads share the looking up of pages.  Whether the other row has a position is
-// read from its bitmap in LDS, kPickBits positions at a time; rows that name a
-// position twice share nothing.  Positions out of the sequence and on pages
+// The selections of R neighbouring rows of a sequence as one list of cache slots
+// (page id * page size + slot), each with the rows that have it: first what all
+// of them have, then row by row what no row before has, in the rows' order.  The
+// rows then share what rows_kernel reads and widens of a common position, and
+// all key heads share the looking up of pages.  Which rows have a position is
+// read from their bitmaps in LDS, kPickBits positions at a time; rows that name
+// a position twice share nothing.  Positions out of the sequence and on pages
 // that do not exist are dropped.
-__global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
+template <int R> __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
 {
-    constexpr int KM = kKvPairWidth / kPickThreads;
-    __shared__ __align__(16) uint32_t sm_bits[2][kPickBits / 32];
-    __shared__ int sm_cnt[3][64];
+    constexpr int KM = kKvSharedWidth / kPickThreads;
+    static_assert(R * kKvSharedWidth <= R * kPickBits / 8, "the entries' rows go where the bitmaps were");
+    static_assert(KM * 4 <= 32 && R <= 4, "the rows that have a thread's entries: 4 bits each");
+    typedef uint32_t Words __attribute__((ext_vector_type(R)));
+    __shared__ __align__(16) Words sm_bits[kPickBits / 32];
+    __shared__ int sm_cnt[R + 1][64];
     __shared__ int sm_odd[8];
+    uint32_t *words = reinterpret_cast<uint32_t *>(sm_bits);
     const KvCache &kc = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t slot = p.slot0 + blockIdx.x;
-    const Seq sq = find_seq(kc, p.S, slot, 2, 1);
+    const Seq sq = find_seq(kc, p.S, slot, R, 1);
     const int seq = sq.i, c0 = sq.c0, c1 = sq.c1;
-    const int64_t t0 = (slot - (c0 / 2 + (int64_t)seq)) * 2;
+    const int64_t t0 = (slot - (c0 / R + (int64_t)seq)) * R;
     if (t0 < 0 || t0 >= c1 - c0) return;
     const int len = clamped(sq.len, (int64_t)kc.table_width << kc.page_shift);
     const int64_t row0 = c0 + t0;
-    const bool two = t0 + 1 < c1 - c0;
+    const int rows = (int)(c1 - c0 - t0 < R ? c1 - c0 - t0 : R);
     const int most = len > 0 ? p.W : 0;   // no token: nothing to look up
-    const int cnt[2] = {clamped(p.valid_len[row0], most),
-                        two ? clamped(p.valid_len[row0 + 1], most) : 0};
+    int cnt[R], some = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        cnt[r] = r < rows ? clamped(p.valid_len[row0 + r], most) : 0;
+        some += cnt[r] > 0;
+    }
     const int base = p.idx0 ? p.idx0[seq] : 0;
     const int32_t *table = kc.table + (int64_t)seq * kc.table_stride;
 
-    int pos[2][KM];                     // -1: no such position
-    uint32_t at[2][KM];                 // its cache slot
-    uint32_t here[2] = {0, 0};          // bit k: entry tid + 256 k has one
+    int pos[R][KM];                     // -1: no such position
+    uint32_t at[R][KM];                 // its cache slot
+    uint32_t here[R] = {};              // bit k: entry tid + 512 k has one
+    uint32_t with[R] = {};              // bits 4 k ..: the rows that have it
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int32_t *src = p.idx + (row0 + (two ? r : 0)) * p.W;
+    for (int r = 0; r < R; ++r) {
+        const int32_t *src = p.idx + (row0 + (r < rows ? r : 0)) * p.W;
         const int last = cnt[r] > 0 ? cnt[r] - 1 : 0;   // loads without branches between them
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
@@ -652,7 +670,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
         }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
             at[r][k] = 0xffffffffu;
@@ -666,7 +684,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
             at[r][k] = (uint32_t)table[in ? x >> kc.page_shift : 0];
         }
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
             if (at[r][k] >= kc.pages) pos[r][k] = -1;
@@ -675,52 +693,64 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
                        ((uint32_t)pos[r][k] & ((1u << kc.page_shift) - 1));
         }
 
-    uint32_t both[2] = {0, 0};          // bit k: the other row has the position too
     bool twice = false;
-    if (cnt[0] > 0 && cnt[1] > 0) {
+    if (some > 1) {
         for (int w0 = 0; w0 < len; w0 += kPickBits) {
             if (w0 > 0) __syncthreads();
-            for (int i = tid; i < 2 * kPickBits / 128; i += kPickThreads)
+            for (int i = tid; i < kPickBits / 32 * R / 4; i += kPickThreads)
                 reinterpret_cast<uint4 *>(sm_bits)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int k = 0; k < KM; ++k) {
                     const uint32_t x = (uint32_t)(pos[r][k] - w0);
                     if (kPickThreads * k < cnt[r] && pos[r][k] >= 0 && x < (uint32_t)kPickBits)
-                        twice |= atomicOr(&sm_bits[r][x >> 5], 1u << (x & 31)) >> (x & 31) & 1;
+                        twice |= atomicOr(&words[(x >> 5) * R + r], 1u << (x & 31)) >> (x & 31) & 1;
                 }
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int k = 0; k < KM; ++k) {
                     const uint32_t x = (uint32_t)(pos[r][k] - w0);
-                    if (kPickThreads * k < cnt[r] && pos[r][k] >= 0 && x < (uint32_t)kPickBits)
-                        both[r] |= (sm_bits[r ^ 1][x >> 5] >> (x & 31) & 1) << k;
+                    if (kPickThreads * k < cnt[r] && pos[r][k] >= 0 && x < (uint32_t)kPickBits) {
+                        const Words w = sm_bits[x >> 5];
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int o = 0; o < R; ++o) m |= (w[o] >> (x & 31) & 1) << o;
+                        with[r] |= m << (4 * k);
+                    }
                 }
         }
     }
     const bool any = __ballot(twice) != 0;
     if (lane == 0) sm_odd[wave] = any;
     __syncthreads();
-    bool apart = false;
+    bool apart = some <= 1;
 #pragma unroll
     for (int w = 0; w < 8; ++w) apart |= sm_odd[w] != 0;
-    if (apart) both[0] = both[1] = 0;
     __syncthreads();
-    if (!two) both[0] = ~0u;            // no second row: nothing to keep apart
-    const uint32_t list[3] = {here[0] & both[0], here[0] & ~both[0], here[1] & ~both[1]};
+    const uint32_t full = (1u << rows) - 1;
+    uint32_t list[R + 1] = {};          // bit k: entry tid + 512 k belongs to the list
 #pragma unroll
-    for (int l = 0; l < 3; ++l)
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            if (apart) with[r] = (with[r] & ~(15u << (4 * k))) | 1u << (4 * k + r);
+            const uint32_t m = with[r] >> (4 * k) & 15;
+            if ((here[r] >> k & 1) && (m & ((1u << r) - 1)) == 0)
+                list[r == 0 && m == full ? 0 : r + 1] |= 1u << k;
+        }
+#pragma unroll
+    for (int l = 0; l <= R; ++l)
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
             const int c = __popcll(__ballot(list[l] >> k & 1));
             if (lane == 0) sm_cnt[l][8 * k + wave] = c;
         }
     __syncthreads();
-    if (wave < 3) {                     // lists' entries before those of (k, wave)
+    if (wave <= R) {                    // lists' entries before those of (k, wave)
         const int c = lane < 8 * KM ? sm_cnt[wave][lane] : 0;
         int sum = c;
 #pragma unroll
@@ -732,20 +762,39 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
         if (lane == 63) sm_odd[wave] = sum;
     }
     __syncthreads();
-    const int n[3] = {sm_odd[0], sm_odd[1], sm_odd[2]};
-    uint32_t *out = p.pick + blockIdx.x * 2 * (int64_t)p.W;
+    uint32_t *out = p.pick + (int64_t)blockIdx.x * R * p.W;
+    uint8_t *rows_of = reinterpret_cast<uint8_t *>(sm_bits);   // the bitmaps are done with
     const uint64_t below = (1ull << lane) - 1;
+    int first = 0;
 #pragma unroll
-    for (int l = 0; l < 3; ++l) {
-        const int first = l == 0 ? 0 : l == 1 ? n[0] : n[0] + n[1];
+    for (int l = 0; l <= R; ++l) {
+        const int r = l == 0 ? 0 : l - 1;
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
             const bool mine = list[l] >> k & 1;
             const uint64_t b = __ballot(mine);
-            if (mine) out[first + sm_cnt[l][8 * k + wave] + __popcll(b & below)] = at[l == 2][k];
+            if (mine) {
+                const int to = first + sm_cnt[l][8 * k + wave] + __popcll(b & below);
+                out[to] = at[r][k];
+                rows_of[to] = (uint8_t)(with[r] >> (4 * k) & 15);
+            }
+        }
+        first += sm_odd[l];
+    }
+    __syncthreads();
+    const int row_words = (R * p.W + 31) >> 5;
+    uint32_t *out_rows = p.pick_rows + (int64_t)blockIdx.x * R * row_words;
+    for (int i = 64 * wave; i < first; i += kPickThreads) {
+        const uint32_t m = i + lane < first ? rows_of[i + lane] : 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t b = __ballot(m >> r & 1);
+            const int w = (i >> 5) + lane;          // the last one may be past the row's words
+            if (lane < 2 && w < row_words)
+                out_rows[r * row_words + w] = (uint32_t)(lane ? b >> 32 : b);
         }
     }
-    if (tid == 0) p.pick_n[blockIdx.x] = make_int4(n[0], n[1], n[2], 0);
+    if (tid == 0) p.pick_n[blockIdx.x] = first;
 }
 
 template <bool FP8, int D>
@@ -754,7 +803,7 @@ hipError_t launch_rows(int nt, const KvAttendParams &p, hipStream_t st)
     const dim3 g((uint32_t)kv_blocks(p)), b(256);
 #define ROWS(NT)                                                                  \
     case NT:                                                                      \
-        if (p.pick) rows_kernel<FP8, D, NT, kPairs><<<g, b, 0, st>>>(p);          \
+        if (p.pick) rows_kernel<FP8, D, NT, kShared><<<g, b, 0, st>>>(p);          \
         else if (p.idx) rows_kernel<FP8, D, NT, kSelected><<<g, b, 0, st>>>(p);   \
         else rows_kernel<FP8, D, NT, kAll><<<g, b, 0, st>>>(p);                   \
         break
@@ -779,7 +828,10 @@ hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hip
 
 hipError_t launch_kv_pick(const KvAttendParams &p, hipStream_t st)
 {
-    pick_kernel<<<dim3((uint32_t)p.slots), kPickThreads, 0, st>>>(p);
+    const dim3 g((uint32_t)p.slots);
+    if (p.tile_rows == 2) pick_kernel<2><<<g, kPickThreads, 0, st>>>(p);
+    else if (p.tile_rows == 4) pick_kernel<4><<<g, kPickThreads, 0, st>>>(p);
+    else return hipErrorInvalidValue;
     return hipGetLastError();
 }
 

@@ -424,12 +424,16 @@ SELECTED = [
 
 
 PAIRS = [
-    # many rows and few heads a key head: two neighbouring rows share their positions
+    # many rows and few heads a key head: two or four neighbouring rows share their positions
     (FP8, 128, 64, 8, 8, [300], [151], 65),
     (BF16, 64, 16, 4, 5, [333, 41, 0, 200], [160, 41, 3, 101], 40),
     (FP8, 64, 32, 16, 16, [500, 90], [64, 3], 129),
     (BF16, 128, 128, 2, 3, [700], [513], 70),
     (FP8, 128, 16, 1, 1, [260, 300], [512, 515], 33),
+    (BF16, 64, 32, 8, 4, [600, 0, 70], [258, 5, 2], 70),
+    (FP8, 64, 16, 8, 3, [1700], [261], 1500),                    # several lists of entries
+    (FP8, 128, 16, 16, 8, [400, 30], [515, 6], 37),              # four rows in 32 columns
+    (BF16, 128, 64, 16, 6, [300], [700], 21),
 ]
 
 

@@ -153,11 +153,12 @@ def test_workspace_is_asked_for_exactly_when_rows_are_split():
     sel = lambda S, W: (lib.indexer_kv_attend_selected_workspace_bytes(  # noqa: E731
         cache(), wide, S, 16, W, ctypes.byref(n)), n.value)
     assert sel(1, 200) == (0, 0) and sel(4096, 5000) == (0, 0)
-    # many rows: lists of two rows' positions (2 W entries and their counts), at
-    # most 256 MB of them at a time
-    pairs = 4096 // 2 + 1
-    assert sel(4096, 2048) == (0, pairs * (2 * 2048 * 4 + 16))
-    assert sel(10 ** 6, 2048)[1] <= 2 ** 28 < sel(10 ** 6, 2048)[1] + 2 * 2048 * 4 + 16 + 256
+    # many rows: lists of 2 or 4 rows' positions (4 bytes and a bit for each row an
+    # entry, a count), at most 256 MB of them at a time
+    group = lambda rows: rows * 2048 * 4 + rows * rows * 2048 // 8 + 4  # noqa: E731
+    assert sel(2048, 2048) == (0, (2048 // 2 + 1) * group(2))
+    assert sel(4096, 2048) == (0, (4096 // 4 + 1) * group(4))
+    assert sel(10 ** 6, 2048)[1] <= 2 ** 28 < sel(10 ** 6, 2048)[1] + group(4)
     rc, few = sel(1, 2048)
     assert rc == 0 and few > 0
     assert selected(s=wide, S=1, q_heads=16, W=2048) == _lib.IDX_EWORKSPACE
