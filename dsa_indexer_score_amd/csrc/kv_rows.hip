@@ -34,7 +34,7 @@
 // 64 rows of up to 16,384 keys 238 us, 4.7 TB/s.  With few keys it is the chain of
 // dependent loads (sequence, page, row): 5.5 us for 128 keys, 0.9 us for each 128
 // more in a block.  2,048 rows with 2,048 selected positions each (64 / 8 heads)
-// take 475 us, with 32 / 8 heads 322: the vector unit, which widens 256 codes of a
+// take 452 us, with 32 / 8 heads 305: the vector unit, which widens 256 codes of a
 // position for 16 columns, is busy for more than half of it, the matrix unit for
 // some 16 %, and they overlap little.
 #include "kv_common.h"
@@ -45,7 +45,7 @@ namespace {
 constexpr int kList = 1024;             // keys resolved to rows at a time
 constexpr uint32_t kNoPage = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 of the largest probability against the running maximum
-constexpr int kPickThreads = 512;       // kKvSharedWidth / 512 entries of a row each
+constexpr int kPickThreads = 512;
 constexpr int kPickBits = 1 << 17;      // positions that a row's bitmap covers at a time
 constexpr int kFewParts = 16;           // parts that one wave joins
 constexpr float kLn2 = 0.693147180559945309f;
@@ -624,13 +624,18 @@ __global__ __launch_bounds__(T) void join_kernel(KvAttendParams p)
 // read from their bitmaps in LDS, kPickBits positions at a time; rows that name
 // a position twice share nothing.  Positions out of the sequence and on pages
 // that do not exist are dropped.
-template <int R> __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvAttendParams p)
+//
+// KM: entries of a row and thread.  Bound by latency, so two blocks a CU where
+// the entries leave the registers for it (512 blocks of four rows of 2,048
+// positions: 25 us, with KM = 8, one block a CU, 43).
+template <int R, int KM>
+__global__ __launch_bounds__(kPickThreads, R * KM <= 20 ? 4 : 2)
+void pick_kernel(KvAttendParams p)
 {
-    constexpr int KM = kKvSharedWidth / kPickThreads;
-    static_assert(R * kKvSharedWidth <= R * kPickBits / 8, "the entries' rows go where the bitmaps were");
+    static_assert(KM * kPickThreads <= kPickBits / 8, "the entries' rows go where the bitmaps were");
     static_assert(KM * 4 <= 32 && R <= 4, "the rows that have a thread's entries: 4 bits each");
     typedef uint32_t Words __attribute__((ext_vector_type(R)));
-    __shared__ __align__(16) Words sm_bits[kPickBits / 32];
+    __shared__ __align__(16) Words sm_bits[kPickBits / 32 + 4];
     __shared__ int sm_cnt[R + 1][64];
     __shared__ int sm_odd[8];
     uint32_t *words = reinterpret_cast<uint32_t *>(sm_bits);
@@ -697,7 +702,8 @@ template <int R> __global__ __launch_bounds__(kPickThreads) void pick_kernel(KvA
     if (some > 1) {
         for (int w0 = 0; w0 < len; w0 += kPickBits) {
             if (w0 > 0) __syncthreads();
-            for (int i = tid; i < kPickBits / 32 * R / 4; i += kPickThreads)
+            const int bits = len - w0 < kPickBits ? len - w0 : kPickBits;
+            for (int i = tid; i < (bits + 31) / 32 * R / 4 + 1; i += kPickThreads)
                 reinterpret_cast<uint4 *>(sm_bits)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
 #pragma unroll
@@ -829,8 +835,11 @@ hipError_t launch_kv_rows(int dtype, int d, int nt, const KvAttendParams &p, hip
 hipError_t launch_kv_pick(const KvAttendParams &p, hipStream_t st)
 {
     const dim3 g((uint32_t)p.slots);
-    if (p.tile_rows == 2) pick_kernel<2><<<g, kPickThreads, 0, st>>>(p);
-    else if (p.tile_rows == 4) pick_kernel<4><<<g, kPickThreads, 0, st>>>(p);
+    const bool wide = p.W > 5 * kPickThreads;
+    if (p.tile_rows == 2 && wide) pick_kernel<2, 8><<<g, kPickThreads, 0, st>>>(p);
+    else if (p.tile_rows == 2) pick_kernel<2, 5><<<g, kPickThreads, 0, st>>>(p);
+    else if (p.tile_rows == 4 && wide) pick_kernel<4, 8><<<g, kPickThreads, 0, st>>>(p);
+    else if (p.tile_rows == 4) pick_kernel<4, 5><<<g, kPickThreads, 0, st>>>(p);
     else return hipErrorInvalidValue;
     return hipGetLastError();
 }
