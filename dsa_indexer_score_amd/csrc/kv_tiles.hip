@@ -23,7 +23,11 @@
 // otherwise, like the values of a bf16 cache.  The running maximum moves only
 // when a score exceeds it by more than 2^8, so that O is rarely rescaled; the
 // probabilities are at most 2^8 then, in fp32 sums and bf16 operands that lose
-// nothing by it.
+// nothing by it.  At d = 128 the maximum is not even computed unless a lane's 32
+// probabilities of a tile add up to more than 2^13 against the present one (1.98
+// -> 1.87 ms for the chunk below); the scores have to be kept for that, and at d =
+// 64, where four waves share a SIMD's registers, that costs more than the maximum
+// (134 -> 243 us for five packed prompts).
 //
 // Bound by the matrix unit and the exponentials beside it, which overlap little:
 // 4,096 rows behind 28,672 keys (e4m3, d = 128, 32 / 8 heads) take 1.95 to 2.05
@@ -42,6 +46,7 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kTile = 64;  // keys
 constexpr int kRanked = 16;     // sequences whose tiles are ranked
 constexpr float kSlack = 8.0f;  // log2 of the largest probability against the running maximum
+constexpr float kMost = 8192.0f;  // of a lane's probabilities of a tile against it, unless the maximum is looked for
 
 template <bool HI> __device__ inline uint32_t widen_scaled(uint32_t w, float s)
 {
@@ -135,6 +140,7 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
     constexpr int KC = D * ES / 16;     // 16-byte chunks of a key in memory
     constexpr int VQ = D / 4;           // groups of four channels
     constexpr uint32_t RB = D * ES;     // bytes of a row
+    constexpr bool LAZY = D == 128;
     __shared__ uint4 kf[2][2 * KS * 64];
     __shared__ uint4 vf[2][4 * DT * 64];
     __shared__ __align__(16) float sm_ks[2][4];  // factor of each 16 keys' scores; < 0: not there
@@ -176,8 +182,8 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
     // ---- the lane's column
     const int col = wave * 32 + n, tok = col / gsize, hh = grp * gsize + col % gsize;
     const bool in = tok < ntok && hh < p.group;
-    int own = len;                       // keys that the column sees
-    if (p.causal) {
+    int own = in ? len : 0;              // keys that the column sees
+    if (in && p.causal) {
         const int64_t x = (int64_t)len - rows_in_seq + t0 + tok + 1;
         own = x < 0 ? 0 : x < len ? (int)x : len;
     }
@@ -403,34 +409,58 @@ __global__ __launch_bounds__(512, D == 64 ? 4 : 2) void tiles_kernel(KvAttendPar
                     if (at + key >= own || (miss >> (key >> 4) & 1)) s[kt][j] = -__builtin_inff();
                 }
         }
-        float top = -__builtin_inff();       // factors are positive, so maxima carry over
+        auto maximum = [&]() KV_INLINE {     // factors are positive, so maxima carry over
+            float top = -__builtin_inff();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            float m = s[x >> 1][8 * (x & 1)];
+            for (int x = 0; x < 4; ++x) {
+                float m = s[x >> 1][8 * (x & 1)];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) m = fmaxf(m, s[x >> 1][8 * (x & 1) + j]);
-            top = fmaxf(top, m * ks[x]);
-        }
-        top = max_over_halves(top);
-        if (__ballot(top > mx + kSlack)) {   // also the first tile: mx = -inf
+                for (int j = 1; j < 8; ++j) m = fmaxf(m, s[x >> 1][8 * (x & 1) + j]);
+                top = fmaxf(top, m * ks[x]);
+            }
+            return max_over_halves(top);
+        };
+        auto raise = [&](float top) KV_INLINE {
             const float m2 = fmaxf(mx, top);
             const float a = mx == m2 ? 1.0f : __builtin_amdgcn_exp2f(mx - m2);
             mx = m2;
             l *= a;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= a;
-        }
-        const float m1 = mx == -__builtin_inff() ? 0.0f : mx;
+        };
+        float sum;
+        auto probabilities = [&]() KV_INLINE {
+            const float m1 = mx == -__builtin_inff() ? 0.0f : mx;
+            sum = LAZY ? 0.0f : l;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            float e[8];
+            for (int x = 0; x < 4; ++x) {
+                float e[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + j], ks[x], -m1));
-                l += e[j];
+                for (int j = 0; j < 8; ++j) {
+                    e[j] = __builtin_amdgcn_exp2f(
+                        __builtin_fmaf(s[x >> 1][8 * (x & 1) + j], ks[x], -m1));
+                    sum += e[j];
+                }
+                pk[x] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
+                                   pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
             }
-            pk[x] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
-                               pack_bf16(e[6], e[7]));
+        };
+        if constexpr (LAZY) {
+            bool again = __ballot(mx == -__builtin_inff() && own > at) != 0;  // first keys
+            if (!again) {
+                probabilities();
+                again = __ballot(sum > kMost) != 0;
+            }
+            if (again) {
+                raise(maximum());
+                probabilities();
+            }
+            l += sum;
+        } else {
+            const float top = maximum();
+            if (__ballot(top > mx + kSlack)) raise(top);   // also the first tile: mx = -inf
+            probabilities();
+            l = sum;
         }
         asm volatile("" : "+v"(l));          // summed here, not behind the matrix phase
     };

@@ -343,6 +343,27 @@ def test_factors_that_underflow_leave_masked_positions_masked(c):
     check(out, lse, ref, d, "underflow")
 
 
+@pytest.mark.parametrize("step", [1, -1], ids=["growing", "shrinking"])
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [FP8, BF16])
+def test_scores_that_double_from_page_to_page(dtype, d, rows, step):
+    """Later keys that leave the first ones' maximum far behind (up to some 2^12,
+    beyond any exponent's range), and the other way round."""
+    L, page = 750, 64
+    pr = Problem(17, dtype, 1, d, page, [L])
+    for j in range(-(-L // page)):
+        f = np.float32(2.0 ** (j if step > 0 else 11 - j))
+        kind = pr.scale if dtype == FP8 else pr.cache
+        kind["k"][pr.table[0, j]] *= f
+    cu = np.array([0, rows], np.int32)
+    q = pr.queries(rows, 8)
+    ref = okv.attend(q.double().numpy(), cu, pr.lens, pr.table, pr.cache["k"], pr.scale["k"],
+                     pr.cache["v"], pr.scale["v"], d ** -0.5)
+    out, lse = pr.gpu().attend(q.to(DEV), dev(cu), dev(pr.lens), dev(pr.table), with_lse=True)
+    check(out, lse, ref, d, f"{rows} rows")
+
+
 @pytest.mark.parametrize("rows,group", [(1, 1), (1, 128)], ids=["rows", "tiles"])
 def test_a_sequence_of_nearly_2_31_positions(rows, group):
     """All pages but the last are page 0 (score 0, value 1), the last is page 1
