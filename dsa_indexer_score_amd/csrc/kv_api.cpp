@@ -149,10 +149,10 @@ constexpr int kTilesHeads = 64;       // query heads of a key head in a block of
 // positions; more rows take several launches.
 constexpr int64_t kPickBytes = int64_t(1) << 28;
 // Four rows share their selections rather than two where that fills 16 columns
-// that two leave empty (2,048 rows x 2,048 of 65,536, 32 / 8 heads, e4m3: 305 us
-// against 455), or, with 5 to 8 heads a key head, takes 32 columns in place of 16
-// and leaves several rounds of blocks (64 / 8 heads: 456 against 473, bf16 521
-// against 624; 777 rows of 4 key heads, one round: 96 against 90).
+// that two leave empty (2,048 rows x 2,048 of 65,536, 32 / 8 heads, e4m3: 283 us
+// against 412), or, with 5 to 8 heads a key head, takes 32 columns in place of 16
+// and leaves several rounds of blocks (64 / 8 heads: 420 against 426, bf16 509
+// against 607; 777 rows of 4 key heads, one round: 93 against 90).
 constexpr int64_t kManyBlocks = 2048;
 constexpr int64_t kMinTileChunk = 512;
 

@@ -3,9 +3,12 @@
 //
 //   o = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
 //
-// One pass over the keys with the running maximum m and sum l of each row; the
-// scores are kept in base 2 (scale * log2 e, times the key page's scale, is one
-// fp32 factor on the exact bf16 products that the matrix unit sums in fp32).
+// One pass over the keys with a reference m and the sum l of each row; the scores
+// are kept in base 2 (scale * log2 e, times the key page's scale, is one fp32
+// factor on the exact bf16 products that the matrix unit sums in fp32).  m is the
+// first tile's maximum, and a later one where a lane's 8 probabilities of a tile
+// add up to more than 2^13: between these no maximum is computed (452 -> 434 us
+// for the selections below).
 //
 // A block takes the query rows of one key head (up to 32 columns: rows of a
 // sequence times the head's query heads) and a range of the keys; its four
@@ -34,7 +37,7 @@
 // 64 rows of up to 16,384 keys 238 us, 4.7 TB/s.  With few keys it is the chain of
 // dependent loads (sequence, page, row): 5.5 us for 128 keys, 0.9 us for each 128
 // more in a block.  2,048 rows with 2,048 selected positions each (64 / 8 heads)
-// take 452 us, with 32 / 8 heads 305: the vector unit, which widens 256 codes of a
+// take 434 us, with 32 / 8 heads 283: the vector unit, which widens 256 codes of a
 // position for 16 columns, is busy for more than half of it, the matrix unit for
 // some 16 %, and they overlap little.
 #include "kv_common.h"
@@ -44,7 +47,7 @@ namespace {
 
 constexpr int kList = 1024;             // keys resolved to rows at a time
 constexpr uint32_t kNoPage = 0xffffffffu;
-constexpr float kSlack = 8.0f;          // log2 of the largest probability against the running maximum
+constexpr float kMost = 8192.0f;        // of a lane's probabilities of a tile against the reference
 constexpr int kPickThreads = 512;
 constexpr int kPickBits = 1 << 17;      // positions that a row's bitmap covers at a time
 constexpr int kFewParts = 16;           // parts that one wave joins
@@ -288,13 +291,14 @@ void rows_kernel(KvAttendParams p)
     }
     minlim = uniform(minlim);
 
-    // The running maximum is ref, once thr is not -inf; before, nothing was seen.
+    // The reference that the probabilities are taken against, once a key was seen.
     kvf4 o[NT][MT];
-    float ref[NT], thr[NT], l[NT];
+    float ref[NT], l[NT];
+    bool seen[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         ref[t] = 0.0f;
-        thr[t] = -__builtin_inff();
+        seen[t] = false;
         l[t] = 0.0f;
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[t][i] = kvf4{0, 0, 0, 0};
@@ -358,29 +362,43 @@ void rows_kernel(KvAttendParams p)
                     if ((bad >> key & 1) || (ALL && s0 + at + key >= lim[t])) x[j] = -__builtin_inff();
                 }
             }
-            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                              fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            top = max_over_rows(top);
-            if (__ballot(top > thr[t])) {          // also the first tile
+            float y[8], sum;
+            auto probabilities = [&]() KV_INLINE {
+                sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = __builtin_amdgcn_exp2f(x[j]);
+                    sum += y[j];
+                }
+            };
+            bool again = __ballot(!seen[t]) != 0;
+            if (!again) {
+                probabilities();
+                again = __ballot(sum > kMost) != 0;
+            }
+            if (again) {                 // a new reference: the maximum, if it is more
+                float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                                  fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                top = max_over_rows(top);
                 const bool some = top > -__builtin_inff();
-                const float up = thr[t] > 0.0f ? fmaxf(top, 0.0f) : some ? top : 0.0f;
-                const float a = __builtin_amdgcn_exp2f(thr[t] > 0.0f ? -up : 0.0f);
+                const float up = seen[t] ? fmaxf(top, 0.0f) : some ? top : 0.0f;
+                const float a = __builtin_amdgcn_exp2f(seen[t] ? -up : 0.0f);
                 ref[t] += up;
-                thr[t] = some ? kSlack : thr[t];
+                seen[t] |= some;
                 l[t] *= a;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[t][i] *= a;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] -= up;
+                probabilities();
             }
+            l[t] += sum;
+            if constexpr (FP8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = __builtin_amdgcn_exp2f(x[j]);
-                l[t] += x[j];
-                if constexpr (FP8) x[j] *= vs[j];
+                for (int j = 0; j < 8; ++j) y[j] *= vs[j];
             }
-            pk[t] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                               pack_bf16(x[6], x[7]));
+            pk[t] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                               pack_bf16(y[6], y[7]));
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -470,7 +488,7 @@ void rows_kernel(KvAttendParams p)
     float f[NT], mx[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        mx[t] = thr[t] > 0.0f ? ref[t] : -__builtin_inff();
+        mx[t] = seen[t] ? ref[t] : -__builtin_inff();
         l[t] += __shfl_xor(l[t], 16);
         l[t] += __shfl_xor(l[t], 32);
         if (g == 0) {
