@@ -30,8 +30,8 @@
 // (134 -> 243 us for five packed prompts).
 //
 // Bound by the matrix unit and the exponentials beside it, which overlap little:
-// 4,096 rows behind 28,672 keys (e4m3, d = 128, 32 / 8 heads) take 1.86 to 1.96
-// ms, 1.1 PFLOP/s (a large matrix product: 1.4); at d = 64, with twice the
+// 4,096 rows behind 28,672 keys (e4m3, d = 128, 32 / 8 heads) take 1.86 to 2.02
+// ms, 1.0 to 1.1 PFLOP/s (a large matrix product: 1.4); at d = 64, with twice the
 // exponentials for each product, 0.55 PFLOP/s.
 #include <type_traits>
 
