@@ -17,7 +17,7 @@ from ._lib import IDX_BF16, IDX_FP8_E4M3
 
 _DTYPE_CODE = {torch.bfloat16: IDX_BF16, torch.float8_e4m3fn: IDX_FP8_E4M3}
 _PAGES = (16, 32, 64, 128)
-_INT32, _BF16 = torch.int32, torch.bfloat16
+_INT32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 _FEW_KEYS = 768
 
 # The current stream's handle without a Stream object around it: a decode step
@@ -183,13 +183,14 @@ class KVCache:
             raise ValueError("cos and sin come together")
         rope_rows = rot = 0
         if cos is not None:
-            if cos.dim() != 2 or cos.shape != sin.shape:
+            shape = cos.shape
+            if len(shape) != 2 or shape != sin.shape:
                 raise ValueError("cos and sin must be [positions, rot / 2]")
-            for name, t in (("cos", cos), ("sin", sin)):
-                if t.dtype is not torch.float32 or t.get_device() != self._gpu or \
-                        not t.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous float32 on {self.device}")
-            rope_rows, rot = cos.shape[0], 2 * cos.shape[1]
+            if cos.dtype is not _F32 or sin.dtype is not _F32 or cos.get_device() != self._gpu or \
+                    sin.get_device() != self._gpu or \
+                    not (cos.is_contiguous() and sin.is_contiguous()):
+                raise ValueError(f"cos and sin must be contiguous float32 on {self.device}")
+            rope_rows, rot = shape[0], 2 * shape[1]
             if rot % 16 or not 16 <= rot <= self.d or rope_rows < 1:
                 raise ValueError(f"the rotated channels must be a multiple of 16, at most {self.d}")
         rq = ro = None
@@ -257,12 +258,13 @@ class KVCache:
                                                              out)
         if idx.dim() != 2 or idx.shape[0] != S or idx.shape[1] < 1 or tuple(valid_len.shape) != (S,):
             raise ValueError("idx must be [S, W] and valid_len [S]")
-        for name, t in (("idx", idx), ("valid_len", valid_len), ("idx0", idx0)):
-            if t is not None and (t.dtype is not _INT32 or t.get_device() != self._gpu or
-                                  not t.is_contiguous()):
-                raise ValueError(f"{name} must be contiguous int32 on {self.device}")
-        if idx0 is not None and tuple(idx0.shape) != (seqs.nseq,):
-            raise ValueError("idx0 must be [nseq]")
+        if idx.dtype is not _INT32 or valid_len.dtype is not _INT32 or \
+                idx.get_device() != self._gpu or valid_len.get_device() != self._gpu or \
+                not (idx.is_contiguous() and valid_len.is_contiguous()):
+            raise ValueError(f"idx and valid_len must be contiguous int32 on {self.device}")
+        if idx0 is not None and (idx0.dtype is not _INT32 or idx0.get_device() != self._gpu or
+                                 not idx0.is_contiguous() or tuple(idx0.shape) != (seqs.nseq,)):
+            raise ValueError(f"idx0 must be contiguous int32 [nseq] on {self.device}")
         W = idx.shape[1]
         args = (self._ref, seqs, rows, S, Hq, scale, idx.data_ptr(), W, valid_len.data_ptr(),
                 _addr(idx0), o.data_ptr(), _addr(lse))
